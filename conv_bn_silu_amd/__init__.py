@@ -5,17 +5,25 @@ The operator runs in hand-written HIP kernels for gfx950 behind a C ABI
 file).  ``binding`` is a thin ctypes layer over that ABI; PyTorch supplies
 device memory and streams only.  The binding is imported lazily so that the
 input generator (``synth``) can be used without the shared library.
+
+``block8`` holds the 8-bit operators of a served transformer block
+(``include/cbs_block8.h``): a linear layer in 8-bit integers, a paged key/value
+cache that quantises what it is given, and attention over it.
 """
 from __future__ import annotations
 
 import importlib
 
-__all__ = ["conv_bn_silu", "conv_bn_silu_unfused", "fold_bn", "binding", "synth"]
+_BLOCK8 = ("int8_linear", "PagedCache", "cache_write", "cache_read", "paged_attention")
+
+__all__ = ["conv_bn_silu", "conv_bn_silu_unfused", "fold_bn", *_BLOCK8, "binding", "block8", "synth"]
 
 
 def __getattr__(name):
-    if name in ("binding", "synth"):
+    if name in ("binding", "block8", "synth"):
         return importlib.import_module(f"{__name__}.{name}")
     if name in ("conv_bn_silu", "conv_bn_silu_unfused", "fold_bn", "Library"):
         return getattr(importlib.import_module(f"{__name__}.binding"), name)
+    if name in _BLOCK8:
+        return getattr(importlib.import_module(f"{__name__}.block8"), name)
     raise AttributeError(name)

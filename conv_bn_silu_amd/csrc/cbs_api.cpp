@@ -13,18 +13,9 @@
 #include <set>
 
 #include "../../include/conv_bn_silu.h"
+#include "cbs_handle.h"
 #include "cbs_launch.h"
 #include "cbs_shape.h"
-
-struct conv_bn_silu_handle {
-    // Fixed at create and only read afterwards, so one handle may serve
-    // concurrent calls from any number of threads and streams.
-    int device;
-    int num_cu;
-    // Device address of the allocation-free entry point's scratch on this
-    // device (NULL if the lookup failed; that entry point then reports it).
-    void *noalloc_scratch;
-};
 
 namespace {
 
@@ -35,10 +26,33 @@ std::set<const conv_bn_silu_handle *> g_handles;  // live handles; never derefer
 // library (kept per thread, so that handles stay read-only).
 thread_local int t_last_hip_error = 0;
 
+}  // namespace
+
+namespace cbs {
+
 bool handle_live(const conv_bn_silu_handle *h) {
     std::lock_guard<std::mutex> lk(g_handles_mu);
     return h != nullptr && g_handles.count(h) != 0;
 }
+
+int check_device(const conv_bn_silu_handle *h) {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return CBS_ERR_NO_DEVICE;
+    return dev == h->device ? CBS_OK : CBS_ERR_INVALID_ARG;  // else the handle belongs to another device
+}
+
+int record_hip(hipError_t e) {
+    if (e == hipSuccess) return CBS_OK;
+    t_last_hip_error = (int)e;
+    return CBS_ERR_HIP;
+}
+
+}  // namespace cbs
+
+namespace {
+
+using cbs::handle_live;
+using cbs::record_hip;
 
 // Geometry and overflow checks; fills `s` on success.
 int check_shape(int N, int C_in, int H, int W, int C_out, int KH, int KW, int stride, int pad,
@@ -175,12 +189,6 @@ hipError_t launch(int variant, const cbs::Shape &s, int dtype, int epi, const vo
     }
 }
 
-int record_hip(hipError_t e) {
-    if (e == hipSuccess) return CBS_OK;
-    t_last_hip_error = (int)e;
-    return CBS_ERR_HIP;
-}
-
 // Common front half of the run entry points: handle, arguments, device.
 int prologue(conv_bn_silu_t h, const void *x, const void *w, const float *scale, const float *bias,
              const void *y, int N, int C_in, int H, int W, int C_out, int KH, int KW, int stride, int pad,
@@ -188,10 +196,7 @@ int prologue(conv_bn_silu_t h, const void *x, const void *w, const float *scale,
     if (!handle_live(h)) return CBS_ERR_BAD_HANDLE;
     const int rc = validate_all(x, w, scale, bias, y, N, C_in, H, W, C_out, KH, KW, stride, pad, dtype, s);
     if (rc != CBS_OK) return rc;
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess) return CBS_ERR_NO_DEVICE;
-    if (dev != h->device) return CBS_ERR_INVALID_ARG;  // the handle belongs to another device
-    return CBS_OK;
+    return cbs::check_device(h);
 }
 
 // The unfused sequence on t1, t2 (validated by the caller): the AUTO

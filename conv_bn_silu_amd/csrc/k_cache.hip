@@ -1,0 +1,166 @@
+// k_cache.hip -- the paged key/value cache: rows quantised (or converted) as they
+// are written, and read back.
+//
+// Both directions are copies with a little arithmetic: bound by HBM (per row of
+// D values: e D + D + 4 bytes each way for 8-bit caches).  A row belongs to a
+// team of 16 lanes (32 when D > 128), 8 elements a lane, so that a lane moves
+// one 16-byte piece of a 16-bit row and the row's largest magnitude is a 4-step
+// exchange inside the team; a workgroup handles 16 (8) rows of k or v and ends: as
+// for the plain copy, many short workgroups keep the most bytes in flight.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "b8_device.h"
+#include "b8_launch.h"
+
+namespace cbs {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct CacheParams {
+    CacheIo io;
+    FastDiv heads, page;
+    uint32_t rows;   // tokens * heads
+    uint32_t slots;  // pages * page size
+};
+
+// Largest over a team of TEAM consecutive lanes, in every lane of it.
+template <int TEAM> __device__ __forceinline__ uint32_t team_max(uint32_t v) {
+#pragma unroll
+    for (int o = 1; o < TEAM; o *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, o, TEAM));
+    return v;
+}
+
+__device__ __forceinline__ int64_t cache_row(const CacheParams &p, uint32_t slot, uint32_t head) {
+    const uint32_t page = p.page.div(slot), off = slot - page * p.page.d;
+    return ((int64_t)page * p.io.cache.heads + head) * p.page.d + off;
+}
+
+template <typename T, bool VEC> __device__ __forceinline__ f32x8 load8_or_1(const T *p) {
+    if constexpr (VEC) {
+        return Value<T>::load8(p);
+    } else {
+        f32x8 x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = Value<T>::load1(p + i);
+        return x;
+    }
+}
+template <typename T, bool VEC> __device__ __forceinline__ void store8_or_1(T *p, f32x8 x) {
+    if constexpr (VEC) {
+        Value<T>::store8(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) Value<T>::store1(p + i, x[i]);
+    }
+}
+
+// T: type of the values given; C: the cache's (int8_t, or a value type).
+// blockIdx.y: 0 keys, 1 values.
+template <typename T, typename C, int TEAM, bool VEC>
+__global__ __launch_bounds__(kThreads) void cache_write(const CacheParams p) {
+    const uint32_t row = blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM;
+    const int d = (int)(threadIdx.x % TEAM) * 8, dim = p.io.cache.dim;
+    const bool second = blockIdx.y != 0;
+    if (row >= p.rows) return;
+    const uint32_t token = p.heads.div(row), head = row - token * p.heads.d;
+    const uint32_t slot = (uint32_t)p.io.slots[token];
+    if (slot >= p.slots) return;  // negative slots are large numbers here
+    const T *src = (const T *)(second ? p.io.v : p.io.k) + token * (second ? p.io.v_token : p.io.k_token) +
+                   head * (second ? p.io.v_head : p.io.k_head);
+    const bool mine = d < dim;
+    f32x8 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (mine) x = load8_or_1<T, VEC>(src + d);
+    const int64_t at = cache_row(p, slot, head);
+    C *dst = (C *)(second ? p.io.cache.v : p.io.cache.k) + at * dim + d;
+    if constexpr (std::is_same_v<C, int8_t>) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, magnitude(x[i]));
+        m = team_max<TEAM>(m);
+        const float s = row_scale(m), inv = row_inverse(s, m);
+        int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (inv != 0.f) row_codes8(x, s, inv, c);
+        if (mine) *(u32x2 *)dst = u32x2{pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])};
+        if (d == 0) (second ? p.io.cache.v_scale : p.io.cache.k_scale)[at] = s;
+    } else {
+        if (mine) Value<C>::store8(dst, x);
+    }
+}
+
+template <typename T, typename C, int TEAM, bool VEC>
+__global__ __launch_bounds__(kThreads) void cache_read(const CacheParams p) {
+    const uint32_t row = blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM;
+    const int d = (int)(threadIdx.x % TEAM) * 8, dim = p.io.cache.dim;
+    const bool second = blockIdx.y != 0;
+    if (row >= p.rows || d >= dim) return;
+    const uint32_t token = p.heads.div(row), head = row - token * p.heads.d;
+    const uint32_t slot = (uint32_t)p.io.slots[token];
+    f32x8 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (slot < p.slots) {
+        const int64_t at = cache_row(p, slot, head);
+        const C *src = (const C *)(second ? p.io.cache.v : p.io.cache.k) + at * dim + d;
+        if constexpr (std::is_same_v<C, int8_t>) {
+            const u32x2 c = *(const u32x2 *)src;
+            const float s = (second ? p.io.cache.v_scale : p.io.cache.k_scale)[at];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = (float)(int8_t)(c[i / 4] >> (8 * (i % 4))) * s;
+        } else {
+            x = Value<C>::load8(src);
+        }
+    }
+    store8_or_1<T, VEC>((T *)(second ? p.io.v_out : p.io.k_out) + (int64_t)row * dim + d, x);
+}
+
+CacheParams params(const CacheIo &a) {
+    return CacheParams{a, make_fastdiv((uint32_t)a.cache.heads), make_fastdiv((uint32_t)a.cache.page_size),
+                       (uint32_t)(a.tokens * a.cache.heads), (uint32_t)(a.cache.pages * a.cache.page_size)};
+}
+
+template <typename T, typename C, int TEAM> hipError_t launch3(const CacheIo &a, bool write, bool vec, hipStream_t st) {
+    const CacheParams p = params(a);
+    const dim3 grid((p.rows + kThreads / TEAM - 1) / (kThreads / TEAM), 2);
+    if (write) {
+        if (vec) cache_write<T, C, TEAM, true><<<grid, kThreads, 0, st>>>(p);
+        else cache_write<T, C, TEAM, false><<<grid, kThreads, 0, st>>>(p);
+    } else {
+        if (vec) cache_read<T, C, TEAM, true><<<grid, kThreads, 0, st>>>(p);
+        else cache_read<T, C, TEAM, false><<<grid, kThreads, 0, st>>>(p);
+    }
+    return hipGetLastError();
+}
+template <typename T, typename C> hipError_t launch2(const CacheIo &a, bool write, bool vec, hipStream_t st) {
+    return a.cache.dim <= 128 ? launch3<T, C, 16>(a, write, vec, st) : launch3<T, C, 32>(a, write, vec, st);
+}
+template <typename T> hipError_t launch1(const CacheIo &a, bool write, bool vec, hipStream_t st) {
+    switch (a.cache.dtype) {
+        case CBS_DTYPE_I8: return launch2<T, int8_t>(a, write, vec, st);
+        case CBS_DTYPE_F32: return launch2<T, float>(a, write, vec, st);
+        case CBS_DTYPE_BF16: return launch2<T, __bf16>(a, write, vec, st);
+        default: return launch2<T, _Float16>(a, write, vec, st);
+    }
+}
+hipError_t launch(const CacheIo &a, bool write, hipStream_t st) {
+    // vector accesses need every row to start at a multiple of 16 bytes
+    const int64_t e = a.dtype == CBS_DTYPE_F32 ? 4 : 2;
+    bool vec;
+    if (write)
+        vec = ((uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)(e * a.k_token) | (uintptr_t)(e * a.k_head) |
+               (uintptr_t)(e * a.v_token) | (uintptr_t)(e * a.v_head)) % 16 == 0;
+    else
+        vec = ((uintptr_t)a.k_out | (uintptr_t)a.v_out) % 16 == 0;  // dim is a multiple of 8
+    switch (a.dtype) {
+        case CBS_DTYPE_F32: return launch1<float>(a, write, vec, st);
+        case CBS_DTYPE_BF16: return launch1<__bf16>(a, write, vec, st);
+        default: return launch1<_Float16>(a, write, vec, st);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_cache_write(const CacheIo &a, hipStream_t st) { return launch(a, true, st); }
+hipError_t launch_cache_read(const CacheIo &a, hipStream_t st) { return launch(a, false, st); }
+
+}  // namespace cbs

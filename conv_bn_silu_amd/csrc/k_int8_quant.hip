@@ -1,0 +1,114 @@
+// k_int8_quant.hip -- the rows of the linear layer's input to 8 bits.
+//
+// Codes are laid out in blocks of 64 along K: code (m, k) at
+// ((k / 64) * rows + m) * 64 + k % 64, with K padded by zero codes to whole
+// 128s, so that the matrix kernels read the fragments of neighbouring rows as
+// contiguous memory and never see past K.
+//
+// Bound by HBM (reads e M K bytes, writes M K).  A row is held in registers
+// between finding its largest magnitude and quantising it, 32 values a lane:
+// one wave per row up to K = 2048, a workgroup of four waves beyond; rows longer
+// than 8192 are read a second time (from L2).
+#include <hip/hip_runtime.h>
+
+#include "b8_device.h"
+#include "b8_linear.h"
+
+namespace cbs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunks = 4;  // of 8 values a lane keeps
+
+template <typename T, bool VEC> __device__ __forceinline__ f32x8 load_chunk(const T *row, int k, int K) {
+    f32x8 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (VEC && k + 8 <= K) return Value<T>::load8(row + k);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (k + i < K) x[i] = Value<T>::load1(row + k + i);
+    return x;
+}
+__device__ __forceinline__ uint32_t chunk_max(f32x8 x) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, magnitude(x[i]));
+    return m;
+}
+__device__ __forceinline__ void store_chunk(int8_t *codes, int rows, int m, int k, f32x8 x, float s, float inv) {
+    int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (inv != 0.f) row_codes8(x, s, inv, c);
+    *(u32x2 *)(codes + ((int64_t)(k >> 6) * rows + m) * 64 + (k & 63)) =
+        u32x2{pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])};
+}
+
+// TEAM lanes per row: 64 or 256.
+template <typename T, bool VEC, int TEAM>
+__global__ __launch_bounds__(kThreads) void quant_rows(const T *__restrict__ x, int64_t x_stride, int M, int K, int Kp,
+                                                       int rows, int8_t *__restrict__ codes,
+                                                       float *__restrict__ scales) {
+    __shared__ uint32_t part[4];
+    const int m = (int)blockIdx.x * (kThreads / TEAM) + (int)threadIdx.x / TEAM;
+    const int lane = (int)threadIdx.x % TEAM;
+    if (TEAM == 64 && m >= M) return;  // with TEAM 256 there is one workgroup per row
+    const T *row = x + (int64_t)m * x_stride;
+    constexpr int kSpan = kChunks * TEAM * 8;
+    f32x8 keep[kChunks];
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        keep[c] = load_chunk<T, VEC>(row, (c * TEAM + lane) * 8, K);
+        top = max(top, chunk_max(keep[c]));
+    }
+    for (int k = kSpan + lane * 8; k < K; k += TEAM * 8) top = max(top, chunk_max(load_chunk<T, VEC>(row, k, K)));
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
+    if constexpr (TEAM == 256) {
+        if (lane % 64 == 0) part[lane / 64] = top;
+        __syncthreads();
+        top = max(max(part[0], part[1]), max(part[2], part[3]));
+    }
+    const float s = row_scale(top), inv = row_inverse(s, top);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int k = (c * TEAM + lane) * 8;
+        if (k < Kp) store_chunk(codes, rows, m, k, keep[c], s, inv);
+    }
+    for (int k = kSpan + lane * 8; k < Kp; k += TEAM * 8)
+        store_chunk(codes, rows, m, k, load_chunk<T, VEC>(row, k, K), s, inv);
+    if (lane == 0) scales[m] = s;
+}
+
+template <typename T, bool VEC> hipError_t launch2(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
+    const T *x = (const T *)a.x;
+    if (a.K <= 2048)
+        quant_rows<T, VEC, 64><<<(a.M + 3) / 4, kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes, l.scales);
+    else
+        quant_rows<T, VEC, 256><<<a.M, kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes, l.scales);
+    return hipGetLastError();
+}
+template <typename T> hipError_t launch1(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
+    const bool vec = ((uintptr_t)a.x | (uintptr_t)(a.x_stride * (int64_t)sizeof(T))) % 16 == 0;
+    return vec ? launch2<T, true>(a, l, st) : launch2<T, false>(a, l, st);
+}
+
+}  // namespace
+
+CodesLayout codes_layout(void *workspace, int64_t M, int64_t K) {
+    CodesLayout l;
+    l.rows = (int)((M + 15) / 16 * 16);
+    l.Kp = (int)((K + 127) / 128 * 128);
+    l.scales = (float *)workspace;
+    l.codes = (int8_t *)workspace + (int64_t)l.rows * 4;
+    l.bytes = (int64_t)l.rows * (4 + l.Kp);
+    return l;
+}
+
+hipError_t launch_quant_rows(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
+    switch (a.dtype) {
+        case CBS_DTYPE_F32: return launch1<float>(a, l, st);
+        case CBS_DTYPE_BF16: return launch1<__bf16>(a, l, st);
+        default: return launch1<_Float16>(a, l, st);
+    }
+}
+
+}  // namespace cbs
