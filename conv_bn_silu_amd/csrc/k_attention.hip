@@ -1,139 +1,98 @@
 // k_attention.hip -- attention of each sequence's newest tokens over its paged
-// cache.
+// cache: how a call is divided between the kernels, and the joining of chunks.
 #include <hip/hip_runtime.h>
 
-#include <type_traits>
-
-#include "b8_device.h"
-#include "b8_launch.h"
+#include "b8_attention.h"
 
 namespace cbs {
 namespace {
 
 constexpr int kThreads = 256;
 
-struct Params {
-    AttentionArgs a;
-    FastDiv page;
-    int group;
+// One row: its chunks' parts, brought to one maximum and added.  A wave to a row.
+template <typename T>
+__device__ __forceinline__ void join(const AttentionPlan &p, const AttentionPart &part, int64_t line, int n, int64_t out) {
+    const int lane = (int)threadIdx.x % 64, dim = p.a.cache.dim;
+    const float *ml = part.ml + 2 * line * part.chunks, *o = part.o + line * part.chunks * dim;
+    float top = -INFINITY;
+    for (int c = 0; c < n; ++c) top = fmaxf(top, ml[2 * c]);
+    float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < n; ++c) {
+        const float f = ml[2 * c] == top ? 1.f : __builtin_amdgcn_exp2f(ml[2 * c] - top);
+        sum += ml[2 * c + 1] * f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (64 * i + lane < dim) v[i] += o[(int64_t)c * dim + 64 * i + lane] * f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (64 * i + lane < dim) Value<T>::store1((T *)p.a.out + out * dim + 64 * i + lane, divide(v[i], sum));
+}
+
+// A workgroup to a sequence and key/value head.
+template <typename T> __global__ __launch_bounds__(kThreads) void join_few(const AttentionPlan p) {
+    const int kvh = (int)blockIdx.x % p.a.cache.heads, wave = (int)threadIdx.x / 64;
+    const Sequence s = sequence(p, (int)blockIdx.x / p.a.cache.heads);
+    const int rows = s.n * (int)p.group.d;
+    if (is_many(p, rows)) return;
+    for (int r = wave; r < rows; r += kThreads / 64) {
+        const int r0 = r / p.few.tile * p.few.tile;
+        const int n = chunks_of(p.few, keys_of(p, s, r0, min(rows, r0 + p.few.tile)));
+        if (n > 1) join<T>(p, p.few, few_line(p, s, kvh, r), n, out_line(p, s, kvh, r));
+    }
+}
+
+int64_t part_floats(const AttentionPart &part, int64_t lines, int64_t dim) {
+    return part.chunks > 1 ? lines * part.chunks * (dim + 2) : 0;
+}
+
+struct Sizes {
+    int64_t batch, tokens, heads, kv_heads, dim, page_size, table_width;
 };
-
-template <typename C> __device__ __forceinline__ f32x8 cache8(const C *p, float s) {
-    if constexpr (std::is_same_v<C, int8_t>) {
-        const u32x2 c = *(const u32x2 *)p;
-        f32x8 x;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (float)(int8_t)(c[i / 4] >> (8 * (i % 4))) * s;
-        return x;
-    } else {
-        return Value<C>::load8(p);
+// The division of a call, and the floats of workspace that it takes.
+int64_t make_plan(AttentionPlan &p, const Sizes &z, int num_cu) {
+    const int64_t group = z.heads / z.kv_heads, limit = z.table_width * z.page_size;
+    // 32 rows only where single tokens do not fill 16: the registers they take cost waves
+    p.few.tile = z.dim <= 128 && (z.tokens > z.batch || group > 16) ? 32 : 16;
+    p.few_only = true;
+    const int64_t pairs = z.batch * z.kv_heads;
+    // up to 1024 keys a second kernel to join chunks costs more than the other CUs save
+    p.few.chunk = (int)(limit <= 1024 ? 1024 : 2048);
+    if (limit > 1024) {
+        const int64_t even = limit * pairs / (16 * num_cu) / 256 * 256;
+        p.few.chunk = (int)(even < 512 ? 512 : even > 1024 ? 1024 : even);
     }
-}
-
-__device__ __forceinline__ float block_reduce(float v, bool is_max, float *tmp) {
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const float w = __shfl_xor(v, o, 64);
-        v = is_max ? fmaxf(v, w) : v + w;
-    }
-    __syncthreads();
-    if (threadIdx.x % 64 == 0) tmp[threadIdx.x / 64] = v;
-    __syncthreads();
-    float r = tmp[0];
-    for (int i = 1; i < kThreads / 64; ++i) r = is_max ? fmaxf(r, tmp[i]) : r + tmp[i];
-    return r;
-}
-
-// One workgroup per query token and head; 256 keys at a time, one a lane, with
-// the running maximum and sum of the softmax.
-template <typename T, typename C> __global__ __launch_bounds__(kThreads) void attend(const Params p) {
-    __shared__ float qs[256], ps[kThreads], tmp[kThreads / 64], part[kThreads / 32][256];
-    __shared__ int64_t rows[kThreads];
-    const AttentionArgs &a = p.a;
-    const int t = (int)threadIdx.x, token = (int)blockIdx.x, head = (int)blockIdx.y, dim = a.cache.dim;
-    int b = 0, first = 0, next = 0;
-    for (; b < a.batch; ++b) {
-        first = max(0, min(a.starts[b], a.tokens));
-        next = max(0, min(a.starts[b + 1], a.tokens));
-        if (token >= first && token < next) break;
-    }
-    if (b == a.batch) return;
-    const int kv_head = head / p.group;
-    const int64_t len = a.lens[b], pos = len - (next - first) + (token - first);
-    const int64_t limit = (int64_t)a.table_width * p.page.d;
-    const int end = (int)max((int64_t)0, min(min(pos + 1, len), limit));
-    const int begin = a.window ? (int)max((int64_t)0, pos + 1 - a.window) : 0;
-    for (int d = t; d < dim; d += kThreads)
-        qs[d] = Value<T>::load1((const T *)a.q + token * a.q_token + head * a.q_head + d) * a.scale;
-    float top = -INFINITY, sum = 0.f;
-    const int dc = t % 32 * 8;  // this lane's values of the output, keys t / 32, + 8, ...
-    f32x8 o = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j0 = begin; j0 < end; j0 += kThreads) {
-        __syncthreads();
-        const int j = j0 + t;
-        float s = -INFINITY;
-        int64_t row = -1;
-        if (j < end) {
-            const uint32_t pg = p.page.div((uint32_t)j);
-            const int page = a.table[b * a.table_stride + pg];
-            if (page >= 0 && page < a.cache.pages) {
-                row = ((int64_t)page * a.cache.heads + kv_head) * p.page.d + (j - (int)(pg * p.page.d));
-                const float ks = std::is_same_v<C, int8_t> ? a.cache.k_scale[row] : 1.f;
-                s = 0.f;
-                for (int d = 0; d < dim; d += 8) {
-                    const f32x8 k = cache8<C>((const C *)a.cache.k + row * dim + d, ks);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(qs[d + i], k[i], s);
-                }
-            }
-        }
-        rows[t] = row;
-        const float new_top = fmaxf(top, block_reduce(s, true, tmp));
-        const float e = row < 0 ? 0.f : __expf(s - new_top);
-        ps[t] = e;
-        const float fade = new_top == -INFINITY ? 1.f : __expf(top - new_top);
-        sum = sum * fade + block_reduce(e, false, tmp);
-        top = new_top;
-        if (dc < dim) {
-            o *= fade;
-            for (int i = t / 32; i < kThreads; i += kThreads / 32) {
-                const int64_t r = rows[i];
-                if (r < 0) continue;
-                const float vs = std::is_same_v<C, int8_t> ? a.cache.v_scale[r] : 1.f;
-                o += cache8<C>((const C *)a.cache.v + r * dim + dc, vs) * ps[i];
-            }
-        }
-    }
-    __syncthreads();
-    if (dc < dim)
-        for (int i = 0; i < 8; ++i) part[t / 32][dc + i] = o[i];
-    __syncthreads();
-    for (int d = t; d < dim; d += kThreads) {
-        float v = 0.f;
-        for (int i = 0; i < kThreads / 32; ++i) v += part[i][d];
-        Value<T>::store1((T *)a.out + ((int64_t)token * a.heads + head) * dim + d, sum > 0.f || sum != sum ? v / sum : 0.f);
-    }
-}
-
-template <typename T> hipError_t launch1(const AttentionArgs &a, hipStream_t st) {
-    const Params p{a, make_fastdiv((uint32_t)a.cache.page_size), a.heads / a.cache.heads};
-    const dim3 grid(a.tokens, a.heads);
-    if (a.cache.dtype == CBS_DTYPE_I8) attend<T, int8_t><<<grid, kThreads, 0, st>>>(p);
-    else attend<T, T><<<grid, kThreads, 0, st>>>(p);
-    return hipGetLastError();
+    p.few.chunks = (int)((limit + p.few.chunk - 1) / p.few.chunk);
+    if (p.few.chunks < 1) p.few.chunks = 1;
+    const int64_t few_lines = p.few_only ? z.tokens * z.heads : pairs * p.few.tile;
+    p.few.o = nullptr;
+    p.few.ml = p.few.o + few_lines * p.few.chunks * z.dim;
+    return part_floats(p.few, few_lines, z.dim);
 }
 
 }  // namespace
 
 int64_t attention_workspace(int num_cu, int64_t batch, int64_t tokens, int heads, int kv_heads, int dim, int page_size,
                             int64_t table_width) {
-    (void)num_cu, (void)batch, (void)tokens, (void)heads, (void)kv_heads, (void)dim, (void)page_size, (void)table_width;
-    return 0;
+    AttentionPlan p{};
+    return 4 * make_plan(p, Sizes{batch, tokens, heads, kv_heads, dim, page_size, table_width}, num_cu);
 }
 
 hipError_t launch_paged_attention(const AttentionArgs &a, int num_cu, hipStream_t st) {
-    (void)num_cu;
-    return a.dtype == CBS_DTYPE_BF16 ? launch1<__bf16>(a, st) : launch1<_Float16>(a, st);
+    AttentionPlan p{};
+    p.a = a;
+    p.page = make_fastdiv((uint32_t)a.cache.page_size);
+    p.group = make_fastdiv((uint32_t)(a.heads / a.cache.heads));
+    make_plan(p, Sizes{a.batch, a.tokens, a.heads, a.cache.heads, a.cache.dim, a.cache.page_size, a.table_width}, num_cu);
+    float *const ws = (float *)a.workspace;
+    const int64_t few_ml = p.few.ml - p.few.o;
+    p.few.o = ws, p.few.ml = ws + few_ml;
+    hipError_t e = launch_attend_few(p, st);
+    if (e != hipSuccess || p.few.chunks == 1) return e;
+    const unsigned grid = (unsigned)(a.batch * a.cache.heads);
+    if (a.dtype == CBS_DTYPE_BF16) join_few<__bf16><<<grid, kThreads, 0, st>>>(p);
+    else join_few<_Float16><<<grid, kThreads, 0, st>>>(p);
+    return hipGetLastError();
 }
 
 }  // namespace cbs
