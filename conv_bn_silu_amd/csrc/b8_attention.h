@@ -54,6 +54,7 @@ struct AttentionPlan {
 };
 hipError_t launch_attend_few(const AttentionPlan &p, hipStream_t st);
 hipError_t launch_attend_many(const AttentionPlan &p, hipStream_t st);
+int many_tile(int64_t dim);  // rows of its tile
 
 #ifdef __HIPCC__
 constexpr float kLog2e = 1.4426950408889634f;
@@ -169,11 +170,6 @@ template <typename X> struct Parts {
         finite = __builtin_bit_cast(x8, f), up = __builtin_bit_cast(x8, u), down = __builtin_bit_cast(x8, d);
     }
 };
-__device__ __forceinline__ float add_infinite(float o, float up, float down) {
-    if (up > 0.f) o += INFINITY;
-    if (down > 0.f) o -= INFINITY;
-    return o;
-}
 
 // A power of two above the scale with these bits (a finite one), at most 2^127.
 __device__ __forceinline__ float power_above(uint32_t bits) {

@@ -2,6 +2,8 @@
 // cache: how a call is divided between the kernels, and the joining of chunks.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "b8_attention.h"
 
 namespace cbs {
@@ -42,32 +44,75 @@ template <typename T> __global__ __launch_bounds__(kThreads) void join_few(const
     }
 }
 
-int64_t part_floats(const AttentionPart &part, int64_t lines, int64_t dim) {
-    return part.chunks > 1 ? lines * part.chunks * (dim + 2) : 0;
+// A wave to a row of the output.
+template <typename T> __global__ __launch_bounds__(kThreads) void join_many(const AttentionPlan p) {
+    const int lane = (int)threadIdx.x % 64;
+    const int64_t line = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+    if (line >= (int64_t)p.a.tokens * p.a.heads) return;
+    const int token = (int)(line / p.a.heads), head = (int)(line - (int64_t)token * p.a.heads);
+    const int kvh = (int)p.group.div((uint32_t)head);
+    for (int b0 = 0; b0 < p.a.batch; b0 += 64) {
+        Sequence s{0, 0, 0, 0};
+        if (b0 + lane < p.a.batch) s = sequence(p, b0 + lane);
+        const uint64_t mine = __ballot(s.first <= token && token < s.first + s.n);
+        if (!mine) continue;
+        s = sequence(p, b0 + __builtin_ctzll(mine));
+        const int rows = s.n * (int)p.group.d, r = (token - s.first) * (int)p.group.d + head - kvh * (int)p.group.d;
+        if (!is_many(p, rows)) return;
+        const int r0 = r / p.many.tile * p.many.tile;
+        const int n = chunks_of(p.many, keys_of(p, s, r0, min(rows, r0 + p.many.tile)));
+        if (n > 1) join<T>(p, p.many, line, n, line);
+        return;
+    }
 }
 
-struct Sizes {
-    int64_t batch, tokens, heads, kv_heads, dim, page_size, table_width;
-};
-// The division of a call, and the floats of workspace that it takes.
-int64_t make_plan(AttentionPlan &p, const Sizes &z, int num_cu) {
-    const int64_t group = z.heads / z.kv_heads, limit = z.table_width * z.page_size;
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+// Lays a kernel's parts out in the workspace, `at` floats of which are taken.
+void place_parts(AttentionPart &part, float *ws, int64_t &at, int64_t lines, int64_t dim) {
+    if (part.chunks <= 1) return;
+    part.o = ws + at;
+    at += lines * part.chunks * dim;
+    part.ml = ws + at;
+    at += lines * part.chunks * 2;
+}
+
+// The division of a call; returns the bytes of workspace that it takes.
+int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
+                  int64_t page_size, int64_t table_width, int64_t num_cu, float *ws) {
+    const int64_t group = heads / kv_heads, limit = table_width * page_size, pairs = batch * kv_heads;
     // 32 rows only where single tokens do not fill 16: the registers they take cost waves
-    p.few.tile = z.dim <= 128 && (z.tokens > z.batch || group > 16) ? 32 : 16;
-    p.few_only = true;
-    const int64_t pairs = z.batch * z.kv_heads;
-    // up to 1024 keys a second kernel to join chunks costs more than the other CUs save
-    p.few.chunk = (int)(limit <= 1024 ? 1024 : 2048);
-    if (limit > 1024) {
-        const int64_t even = limit * pairs / (16 * num_cu) / 256 * 256;
-        p.few.chunk = (int)(even < 512 ? 512 : even > 1024 ? 1024 : even);
+    p.few.tile = dim <= 128 && (tokens > batch || group > 16) ? 32 : 16;
+    p.many.tile = many_tile(dim);
+    // with no more tokens than sequences they are single tokens, as a rule
+    p.few_only = tokens <= batch || tokens * group <= p.few.tile;
+    p.slots = (int)(tokens * group / p.many.tile + std::min(batch, tokens * group / (p.few.tile + 1)));
+
+    // attend_few: 1024 keys are soon read, and joining chunks takes a kernel more.  Beyond,
+    // so many that every CU has several workgroups to its name, but no more than that:
+    // a workgroup needs some steps to fill its pipe.
+    p.few.chunk = (int)std::min<int64_t>(1024, std::max<int64_t>(512, limit * pairs / (16 * num_cu) / 256 * 256));
+    if (limit <= 1024) p.few.chunk = 1024;
+    p.few.chunks = (int)std::max<int64_t>(1, (limit + p.few.chunk - 1) / p.few.chunk);
+
+    // attend_many: chunks only where there are too few tiles for the CUs
+    const int64_t groups = std::max<int64_t>(1, p.slots * kv_heads), want = groups >= num_cu ? 1 : (2 * num_cu + groups - 1) / groups;
+    p.many.chunk = (int)std::max<int64_t>(512, round_up((limit + want - 1) / want, 64));
+    p.many.chunks = (int)std::max<int64_t>(1, (limit + p.many.chunk - 1) / p.many.chunk);
+    if (want == 1) p.many.chunk = 1 << 30, p.many.chunks = 1;
+
+    int64_t at = 0;
+    place_parts(p.few, ws, at, p.few_only ? tokens * heads : pairs * p.few.tile, dim);
+    if (!p.few_only) place_parts(p.many, ws, at, tokens * heads, dim);
+    return 4 * at;
+}
+
+template <typename T> hipError_t launch_joins(const AttentionPlan &p, hipStream_t st) {
+    if (p.few.chunks > 1) join_few<T><<<(unsigned)(p.a.batch * p.a.cache.heads), kThreads, 0, st>>>(p);
+    if (!p.few_only && p.many.chunks > 1) {
+        const int64_t lines = (int64_t)p.a.tokens * p.a.heads;
+        join_many<T><<<(unsigned)((lines + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, st>>>(p);
     }
-    p.few.chunks = (int)((limit + p.few.chunk - 1) / p.few.chunk);
-    if (p.few.chunks < 1) p.few.chunks = 1;
-    const int64_t few_lines = p.few_only ? z.tokens * z.heads : pairs * p.few.tile;
-    p.few.o = nullptr;
-    p.few.ml = p.few.o + few_lines * p.few.chunks * z.dim;
-    return part_floats(p.few, few_lines, z.dim);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -75,7 +120,7 @@ int64_t make_plan(AttentionPlan &p, const Sizes &z, int num_cu) {
 int64_t attention_workspace(int num_cu, int64_t batch, int64_t tokens, int heads, int kv_heads, int dim, int page_size,
                             int64_t table_width) {
     AttentionPlan p{};
-    return 4 * make_plan(p, Sizes{batch, tokens, heads, kv_heads, dim, page_size, table_width}, num_cu);
+    return make_plan(p, batch, tokens, heads, kv_heads, dim, page_size, table_width, num_cu, nullptr);
 }
 
 hipError_t launch_paged_attention(const AttentionArgs &a, int num_cu, hipStream_t st) {
@@ -83,16 +128,12 @@ hipError_t launch_paged_attention(const AttentionArgs &a, int num_cu, hipStream_
     p.a = a;
     p.page = make_fastdiv((uint32_t)a.cache.page_size);
     p.group = make_fastdiv((uint32_t)(a.heads / a.cache.heads));
-    make_plan(p, Sizes{a.batch, a.tokens, a.heads, a.cache.heads, a.cache.dim, a.cache.page_size, a.table_width}, num_cu);
-    float *const ws = (float *)a.workspace;
-    const int64_t few_ml = p.few.ml - p.few.o;
-    p.few.o = ws, p.few.ml = ws + few_ml;
+    make_plan(p, a.batch, a.tokens, a.heads, a.cache.heads, a.cache.dim, a.cache.page_size, a.table_width, num_cu,
+              (float *)a.workspace);
     hipError_t e = launch_attend_few(p, st);
-    if (e != hipSuccess || p.few.chunks == 1) return e;
-    const unsigned grid = (unsigned)(a.batch * a.cache.heads);
-    if (a.dtype == CBS_DTYPE_BF16) join_few<__bf16><<<grid, kThreads, 0, st>>>(p);
-    else join_few<_Float16><<<grid, kThreads, 0, st>>>(p);
-    return hipGetLastError();
+    if (e == hipSuccess && !p.few_only) e = launch_attend_many(p, st);
+    if (e != hipSuccess) return e;
+    return a.dtype == CBS_DTYPE_BF16 ? launch_joins<__bf16>(p, st) : launch_joins<_Float16>(p, st);
 }
 
 }  // namespace cbs

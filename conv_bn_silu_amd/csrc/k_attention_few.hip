@@ -247,14 +247,16 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
 #pragma unroll
             for (int i = 0; i < QT; ++i) {
                 if (!full) {
+                    const uint64_t ahead = valid >> (4 * grp);
+                    const int last = pos[i] - j0 - 4 * grp, first = low[i] - j0 - 4 * grp;
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb) {
                         seen[i][kb] = 0;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int key = 16 * kb + 4 * grp + e, j = j0 + key;
-                            const bool see = ((valid >> key) & 1) && j <= pos[i] && j >= low[i];
-                            seen[i][kb] |= (see ? 1u : 0u) << e;
+                            const int key = 16 * kb + e;  // less 4 grp
+                            const bool see = ((ahead >> key) & 1) && key <= last && key >= first;
+                            seen[i][kb] |= see ? 1u << e : 0u;
                             if (!see) s[i][kb][e] = -INFINITY;
                         }
                     }
@@ -338,7 +340,7 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                             const f32x4 up = mma16(v.up, sight[i][t], f32x4{0.f, 0.f, 0.f, 0.f});
                             const f32x4 down = mma16(v.down, sight[i][t], f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[i][db][e] = add_infinite(o[i][db][e], up[e], down[e]);
+                            for (int e = 0; e < 4; ++e) o[i][db][e] += (up[e] > 0.f ? INFINITY : 0.f) - (down[e] > 0.f ? INFINITY : 0.f);
                         }
                     }
                 }

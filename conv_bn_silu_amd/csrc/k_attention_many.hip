@@ -1,0 +1,470 @@
+// k_attention_many.hip -- paged attention where a sequence has many rows: prompts
+// and their chunks.  The work is the matrix products and the softmax between
+// them.
+//
+// A workgroup takes a tile of rows, 32 to a wave, and goes through the keys 64 at
+// a time.  Keys and values come through registers (where 8-bit codes become fp16,
+// once for all the workgroup's rows) into two LDS buffers, so that one barrier a
+// step suffices: while a step is computed, the loads of the next are on
+// their way, and the page numbers of the one after.  A wave's scores never
+// leave its registers.
+#include <hip/hip_runtime.h>
+
+#include "b8_attention.h"
+
+namespace cbs {
+namespace {
+
+constexpr int KT = 64;  // keys of a step
+
+// NB: dims in 32s.
+template <typename C, int NB> struct ManyShape {
+    static constexpr bool kI8 = std::is_same_v<C, int8_t>;
+    static constexpr int kWaves = NB <= 4 ? 8 : 4;  // dim 256 needs the registers of two waves
+    static constexpr int kThreads = 64 * kWaves, kTile = 32 * kWaves;
+    static constexpr int kPitchDims = NB <= 2 ? 64 : NB <= 4 ? 128 : 256;
+    static constexpr int kPitch = 2 * kPitchDims;                         // bytes of a row in LDS
+    static constexpr int kPieces = kPitchDims * (int)sizeof(C) / 16;      // 16-byte pieces of a row of the cache
+    static constexpr int kRowsPerLoad = kThreads / kPieces;
+    static constexpr int kLoads = kRowsPerLoad < KT ? KT / kRowsPerLoad : 1;
+    static constexpr bool kIdle = kRowsPerLoad > KT;                      // threads without a piece
+    static constexpr int kSide = KT * kPitch;                             // bytes of keys, or of values
+    static constexpr int kOutPitch = kPitch + 16;
+    static constexpr int kOutBytes = kTile * kOutPitch;
+    static constexpr int kBytes = 4 * kSide > kOutBytes ? 4 * kSide : kOutBytes;
+    // Pieces of a row are exchanged: a read of keys takes the same dims of 16 rows at a
+    // time, a transposed read of values 32 dims of 4 rows.
+    static __device__ __forceinline__ int swap_k(int row) { return NB <= 2 ? (row >> 1) & 7 : row & 15; }
+    static __device__ __forceinline__ int swap_v(int row) { return NB <= 2 ? (row & 2) << 1 : (row & 3) << 2; }
+};
+
+// Tile number `slot` of those that attend_many has, over all sequences.
+struct Found {
+    Sequence s;
+    int tile;
+};
+__device__ __forceinline__ bool find_tile(const AttentionPlan &p, int slot, Found &f) {
+    const int lane = (int)threadIdx.x % 64;
+    int before = 0;
+    for (int b0 = 0; b0 < p.a.batch; b0 += 64) {
+        int tiles = 0;
+        if (b0 + lane < p.a.batch) {
+            const int rows = sequence(p, b0 + lane).n * (int)p.group.d;
+            if (is_many(p, rows)) tiles = (rows + p.many.tile - 1) / p.many.tile;
+        }
+        int upto = tiles;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const int x = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += x;
+        }
+        const uint64_t past = __ballot(before + upto > slot);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            f.tile = slot - before - (__shfl(upto, at, 64) - __shfl(tiles, at, 64));
+            f.tile = __builtin_amdgcn_readfirstlane(f.tile);
+            f.s = sequence(p, __builtin_amdgcn_readfirstlane(b0 + at));
+            return true;
+        }
+        before += __shfl(upto, 63, 64);
+    }
+    return false;
+}
+
+// The larger of a lane's value and that of the lane 32 away.
+__device__ __forceinline__ float max_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Zeroes the infinities and NaN among 8 halves; whether there were any.
+template <typename X> __device__ __forceinline__ bool take_out(u32x4 &v) {
+    constexpr uint32_t kExp = std::is_same_v<X, _Float16> ? 0x7C00u : 0x7F80u;
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool lo = (v[e] & kExp) == kExp, hi = ((v[e] >> 16) & kExp) == kExp;
+        v[e] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+        any |= lo || hi;
+    }
+    return any;
+}
+
+template <typename T, typename C, int NB>
+__global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kWaves / 4)) void attend_many(const AttentionPlan p) {
+    using S = ManyShape<C, NB>;
+    using X8 = typename Operand<T, C>::x8;
+    using X = typename Operand<T, C>::type;
+    constexpr int kSteps = 2 * NB;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[S::kBytes];
+    __shared__ __attribute__((aligned(16))) float kscale[2][KT], vscale[2][KT];
+    __shared__ uint64_t valid_bits[2];
+    __shared__ float vrefs[2];
+    __shared__ int bad[2][8];
+    const AttentionArgs &a = p.a;
+    const int tid = (int)threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int col = lane % 32, half = lane / 32;
+    const int hk = a.cache.heads, dim = a.cache.dim;
+    // the key/value head is innermost: with 8 of them each XCD's L2 serves one
+    const int id = (int)blockIdx.x, kvh = id % hk, c = id / hk % p.many.chunks;
+    Found f;
+    // the last tiles of a sequence see the most keys: they go first
+    if (!find_tile(p, p.slots - 1 - id / hk / p.many.chunks, f)) return;
+    const Sequence &seq = f.s;
+    const int rows = seq.n * (int)p.group.d;
+    const int r0 = f.tile * S::kTile, r1 = min(rows, r0 + S::kTile);
+    const Span2 keys = keys_of(p, seq, r0, r1);
+    const int n_chunks = chunks_of(p.many, keys);
+    if (c >= n_chunks) return;
+    const int lo = keys.lo + c * p.many.chunk, hi = min(keys.hi, lo + p.many.chunk);
+    const int old = seq.len - seq.n;
+    // this wave's rows
+    const int w0 = min(r0 + 32 * wave, r1 - 1), w1 = min(r0 + 32 * wave + 31, r1 - 1);
+    const int wave_min = old + (int)p.group.div((uint32_t)w0), wave_max = old + (int)p.group.div((uint32_t)w1);
+    const int wave_low = first_key(p, wave_min), wave_high_low = first_key(p, wave_max);
+
+    const int32_t *const table = a.table + (int64_t)seq.b * a.table_stride;
+    const C *const kdata = (const C *)a.cache.k, *const vdata = (const C *)a.cache.v;
+
+    // this lane's row
+    const int r = min(r0 + 32 * wave + col, r1 - 1), tok = (int)p.group.div((uint32_t)r);
+    const int pos = old + tok, low = first_key(p, pos);
+    float qf = fabsf(a.scale) * kLog2e;
+    X8 q[kSteps];
+    {
+        const T *src = (const T *)a.q + (int64_t)(seq.first + tok) * a.q_token +
+                       (int64_t)(kvh * (int)p.group.d + r - tok * (int)p.group.d) * a.q_head;
+        const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+        u32x4 raw[kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int d = 16 * s + 8 * half;
+            raw[s] = u32x4{0u, 0u, 0u, 0u};
+            if (d < dim) raw[s] = ((const Any16 *)(src + d))->v ^ flip;
+        }
+        if constexpr (std::is_same_v<X, T>) {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(X8, raw[s]);
+        } else {
+            uint32_t top = 0;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max(raw[s][e] & 0x7FFFu, (raw[s][e] >> 16) & 0x7FFFu));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+            const int e = top >= 0x7F80u ? 0 : min(126, 141 - (int)(top >> 7));
+            qf = __builtin_ldexpf(qf, -e);
+            const float up = __builtin_ldexpf(1.f, e);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const bf16x8 v = __builtin_bit_cast(bf16x8, raw[s]);
+#pragma unroll
+                for (int e8 = 0; e8 < 8; ++e8) q[s][e8] = (X)((float)v[e8] * up);
+            }
+        }
+    }
+
+    // Staging: thread's piece of rows my_row, my_row + kRowsPerLoad, ...; the first wave
+    // also looks after the keys as such, one a lane: whether they are there, their scales.
+    const bool my_part = !S::kIdle || tid / S::kPieces < KT;
+    const int my_row = tid / S::kPieces % KT, my_d = tid % S::kPieces * (16 / (int)sizeof(C));
+    const bool my_dims = my_d < dim;
+    u32x4 kreg[S::kLoads], vreg[S::kLoads];
+    bool vok[S::kLoads];
+    int next_page[S::kLoads], key_page = -1;
+    float ks = 0.f, vs = 0.f, vref = 0x1p-126f;
+    uint64_t key_bits = 0;
+    auto page_of = [&](int j) { return j < hi ? table[p.page.div((uint32_t)j)] : -1; };
+    auto row_of = [&](int j, int page, bool &ok) {
+        ok = page >= 0 && page < a.cache.pages;
+        const int off = j - (int)(p.page.div((uint32_t)j) * p.page.d);
+        return ok ? ((int64_t)page * hk + kvh) * (int64_t)p.page.d + off : (int64_t)0;
+    };
+    auto look_up = [&](int j0) {
+#pragma unroll
+        for (int i = 0; i < S::kLoads; ++i) next_page[i] = page_of(j0 + my_row + i * S::kRowsPerLoad);
+        if (wave == 0) key_page = page_of(j0 + lane);
+    };
+    auto load = [&](int j0) {
+#pragma unroll
+        for (int i = 0; i < S::kLoads; ++i) {
+            const int64_t at = row_of(j0 + my_row + i * S::kRowsPerLoad, next_page[i], vok[i]) * dim + (my_dims ? my_d : 0);
+            kreg[i] = *(const u32x4 *)(kdata + at);
+            vreg[i] = *(const u32x4 *)(vdata + at);
+        }
+        if (wave == 0) {
+            bool ok;
+            const int64_t row = row_of(j0 + lane, key_page, ok);
+            key_bits = __ballot(ok);
+            if constexpr (S::kI8) {
+                ks = a.cache.k_scale[row];
+                vs = a.cache.v_scale[row];
+            }
+        }
+    };
+    // Values that only some of the tile's rows see may be infinite or NaN, and zero times
+    // those is no zero: where the step is one that some rows see in part, they are
+    // taken out here and added apart.
+    const int tile_min = old + (int)p.group.div((uint32_t)r0);
+    const int tile_low = first_key(p, old + (int)p.group.div((uint32_t)(r1 - 1)));
+    auto store = [&](int buf, int j0) {
+        unsigned char *const kbuf = lds + buf * 2 * S::kSide, *const vbuf = kbuf + S::kSide;
+        const bool part = j0 + KT - 1 > tile_min || j0 < tile_low;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < S::kLoads; ++i) {
+            const int row = my_row + i * S::kRowsPerLoad;
+            const u32x4 k = kreg[i];
+            if (!my_part) continue;
+            if constexpr (S::kI8) {
+                const u32x4 v = vreg[i];
+                // 16 codes: two pieces of a row in LDS
+                const int piece = 2 * (tid % S::kPieces);
+                unsigned char *const kr = kbuf + row * S::kPitch, *const vr = vbuf + row * S::kPitch;
+                *(f16x8 *)(kr + ((piece ^ S::swap_k(row)) * 16)) = codes_f16(k[0], k[1]);
+                *(f16x8 *)(kr + (((piece + 1) ^ S::swap_k(row)) * 16)) = codes_f16(k[2], k[3]);
+                *(f16x8 *)(vr + ((piece ^ S::swap_v(row)) * 16)) = codes_f16(v[0], v[1]);
+                *(f16x8 *)(vr + (((piece + 1) ^ S::swap_v(row)) * 16)) = codes_f16(v[2], v[3]);
+            } else {
+                const int piece = tid % S::kPieces;
+                // past dim q is zero, and a key's infinity or NaN has no place there
+                const uint32_t kkeep = my_dims ? ~0u : 0u, vkeep = vok[i] ? ~0u : 0u;
+                u32x4 v = vreg[i] & vkeep;
+                if (part) odd |= take_out<X>(v);
+                *(u32x4 *)(kbuf + row * S::kPitch + ((piece ^ S::swap_k(row)) * 16)) = k & kkeep;
+                *(u32x4 *)(vbuf + row * S::kPitch + ((piece ^ S::swap_v(row)) * 16)) = v;
+            }
+        }
+        if constexpr (!S::kI8) {
+            const bool any = __any(odd);
+            if (lane == 0) bad[buf][wave] = any ? 1 : 0;
+        }
+        if (wave == 0) {
+            if constexpr (S::kI8) {
+                const uint32_t bits = magnitude(vs);
+                const bool counts = ((key_bits >> lane) & 1) && bits < 0x7F800000u;
+                if (__any(counts && vs > vref)) {
+                    uint32_t top = counts ? bits : 0u;
+#pragma unroll
+                    for (int x = 1; x < 64; x *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, x, 64));
+                    vref = power_above(top);
+                }
+                kscale[buf][lane] = ks;
+                vscale[buf][lane] = vs * (1.f / vref);
+                if (lane == 0) vrefs[buf] = vref;
+            }
+            if (lane == 0) valid_bits[buf] = key_bits;
+        }
+    };
+
+    f32x16 o[NB] = {};
+    float m = -INFINITY, l = 0.f, o_ref = 0x1p-126f;
+
+    if (lo < hi) {
+        look_up(lo);
+        load(lo);
+        look_up(lo + KT);
+        store(0, lo);
+    }
+    int buf = 0;
+    for (int j0 = lo; j0 < hi; j0 += KT, buf ^= 1) {
+        __syncthreads();
+        const bool more = j0 + KT < hi;
+        if (more) {
+            load(j0 + KT);
+            if (j0 + 2 * KT < hi) look_up(j0 + 2 * KT);
+        }
+        if (j0 <= wave_max && j0 + KT > wave_low) {
+            const unsigned char *const kbuf = lds + buf * 2 * S::kSide, *const vbuf = kbuf + S::kSide;
+            // LDS addresses are made anew for each step: kept, they cost a register for each access
+            int my = lane;
+            asm volatile("" : "+v"(my));
+            const int my_col = my % 32, my_half = my / 32;
+            f32x16 s[2] = {};
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const X8 kf = *(const X8 *)(kbuf + (32 * kb + my_col) * S::kPitch + (((2 * st + my_half) ^ S::swap_k(my_col)) * 16));
+                    s[kb] = mma32(kf, q[st], s[kb]);
+                }
+            const uint64_t valid = valid_bits[buf];
+            const bool full = valid == ~0ull && j0 + KT - 1 <= wave_min && j0 >= wave_high_low;
+            // the lane's keys are 32 kb + 8 g + 4 half + 0..3
+            if constexpr (S::kI8) {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const f32x4 k4 = *(const f32x4 *)(&kscale[buf][32 * kb + 8 * g + 4 * half]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[kb][4 * g + e] *= k4[e];
+                    }
+            }
+            uint32_t seen = ~0u;
+            if (!full) {
+                seen = 0;
+                const uint64_t ahead = valid >> (4 * my_half);
+                const int last = pos - j0 - 4 * my_half, first = low - j0 - 4 * my_half;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int key = 32 * (i / 16) + 8 * (i % 16 / 4) + i % 4;  // less 4 half
+                    const bool see = ((ahead >> key) & 1) && key <= last && key >= first;
+                    seen |= see ? 1u << i : 0u;
+                    if (!see) s[i / 16][i % 16] = -INFINITY;
+                }
+            }
+            float tops[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                tops[x] = fmaxf(s[x / 2][x % 2 * 8], s[x / 2][x % 2 * 8 + 1]);
+#pragma unroll
+                for (int i = 2; i < 8; i += 2)
+                    tops[x] = fmaxf(fmaxf(tops[x], s[x / 2][x % 2 * 8 + i]), s[x / 2][x % 2 * 8 + i + 1]);
+            }
+            const float top = max_halves(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+            const bool move = top > m && !((top - m) * qf <= kSlack);
+            float v_fade = 1.f;
+            if constexpr (S::kI8) {
+                const float ref = vrefs[buf];
+                if (ref != o_ref) v_fade = o_ref / ref, o_ref = ref;
+            }
+            if (__any(move) || v_fade != 1.f) {
+                const float now = move ? top : m;
+                const float fade = move ? (m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - now) * qf)) : 1.f;
+                m = now;
+                l *= fade;
+                const float both = fade * v_fade;
+#pragma unroll
+                for (int db = 0; db < NB; ++db) o[db] *= both;
+            }
+            const float base = m == -INFINITY ? 0.f : m * qf;
+            X8 pr[4];
+            float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    f32x4 v4;
+                    if constexpr (S::kI8) v4 = *(const f32x4 *)(&vscale[buf][32 * kb + 8 * g + 4 * half]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const bool hide = !full && !((seen >> (16 * kb + 4 * g + e)) & 1);
+                        float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][4 * g + e], qf, -base));
+                        if (hide) w = 0.f;
+                        sums[e] += w;
+                        if constexpr (S::kI8) {
+                            w *= v4[e];
+                            if (hide) w = 0.f;  // the scale may be anything
+                        }
+                        pr[2 * kb + g / 2][g % 2 * 4 + e] = (X)w;
+                    }
+                }
+            l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+
+            // values: keys 16 t + 4 half + 0..3 and 8 above those, of dim 32 db + col
+            auto values = [&](int db, int t) {
+                const int row = 16 * t + 4 * my_half + my % 16 / 4, piece = 4 * db + 2 * (my / 16 % 2) + my % 4 / 2;
+                const unsigned char *from = vbuf + row * S::kPitch + ((piece ^ S::swap_v(row)) * 16) + my % 2 * 8;
+                const u32x2 x = read_tr16(from), y = read_tr16(from + 8 * S::kPitch);
+                return u32x4{x.x, x.y, y.x, y.y};
+            };
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int db = 0; db < NB; ++db) o[db] = mma32(__builtin_bit_cast(X8, values(db, t)), pr[t], o[db]);
+            if constexpr (!S::kI8) {
+                int odd = 0;
+#pragma unroll
+                for (int w = 0; w < S::kWaves; ++w) odd |= bad[buf][w];
+                if (odd) {
+                    // the values that store() has taken out, to the rows that see them
+#pragma unroll 1
+                    for (int j = j0; j < min(hi, j0 + KT); ++j) {
+                        bool there;
+                        const int64_t row = row_of(j, table[p.page.div((uint32_t)j)], there);
+                        const bool sees = there && j <= pos && j >= low;
+#pragma unroll
+                        for (int db = 0; db < NB; ++db)
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const int d = 32 * db + 8 * g + 4 * half;
+                                if (d >= dim || !sees) continue;
+                                typedef X x4 __attribute__((ext_vector_type(4)));
+                                const x4 v = *(const x4 *)((const X *)vdata + row * dim + d);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (!__builtin_isfinite((float)v[e])) o[db][4 * g + e] += (float)v[e];
+                            }
+                    }
+                }
+            }
+        }
+        if (more) store(buf ^ 1, j0 + KT);
+    }
+
+    // the lane has one row, of every 32 dims 16
+    const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    const float sum = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+    const int mine = r0 + 32 * wave + col;
+    if (n_chunks > 1) {
+        if (mine >= r1) return;
+        const int64_t line = out_line(p, seq, kvh, mine) * p.many.chunks + c;
+#pragma unroll
+        for (int db = 0; db < NB; ++db)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int d = 32 * db + 8 * g + 4 * half;
+                f32x4 v = {o[db][4 * g], o[db][4 * g + 1], o[db][4 * g + 2], o[db][4 * g + 3]};
+                if constexpr (S::kI8) v *= o_ref;
+                if (d < dim) *(f32x4 *)(p.many.o + line * dim + d) = v;
+            }
+        if (half == 0) p.many.ml[2 * line] = m == -INFINITY ? -INFINITY : m * qf, p.many.ml[2 * line + 1] = sum;
+        return;
+    }
+    __syncthreads();
+    unsigned char *const stage = lds + wave * 32 * S::kOutPitch;
+    const float ref = S::kI8 ? o_ref : 1.f;
+#pragma unroll
+    for (int db = 0; db < NB; ++db)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            typedef T x4 __attribute__((ext_vector_type(4)));
+            x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (T)divide(o[db][4 * g + e] * ref, sum);
+            *(x4 *)(stage + col * S::kOutPitch + 2 * (32 * db + 8 * g + 4 * half)) = v;
+        }
+    __builtin_amdgcn_wave_barrier();
+    constexpr int kOutPieces = S::kPitch / 16;
+#pragma unroll 1
+    for (int i = lane; i < 32 * kOutPieces; i += 64) {
+        const int row = i / kOutPieces, d = i % kOutPieces * 8, at = r0 + 32 * wave + row;
+        if (at < r1 && d < dim)
+            ((Any16 *)((T *)a.out + out_line(p, seq, kvh, at) * dim + d))->v = *(const u32x4 *)(stage + row * S::kOutPitch + 2 * d);
+    }
+}
+
+template <typename T, typename C, int NB> hipError_t launch3(const AttentionPlan &p, hipStream_t st) {
+    const int64_t grid = (int64_t)p.slots * p.many.chunks * p.a.cache.heads;
+    attend_many<T, C, NB><<<(unsigned)grid, ManyShape<C, NB>::kThreads, 0, st>>>(p);
+    return hipGetLastError();
+}
+template <typename T, typename C> hipError_t launch2(const AttentionPlan &p, hipStream_t st) {
+    if (p.a.cache.dim <= 64) return launch3<T, C, 2>(p, st);
+    if (p.a.cache.dim <= 96) return launch3<T, C, 3>(p, st);
+    return p.a.cache.dim <= 128 ? launch3<T, C, 4>(p, st) : launch3<T, C, 8>(p, st);
+}
+template <typename T> hipError_t launch1(const AttentionPlan &p, hipStream_t st) {
+    return p.a.cache.dtype == CBS_DTYPE_I8 ? launch2<T, int8_t>(p, st) : launch2<T, T>(p, st);
+}
+
+}  // namespace
+
+int many_tile(int64_t dim) { return dim <= 128 ? ManyShape<int8_t, 4>::kTile : ManyShape<int8_t, 8>::kTile; }
+
+hipError_t launch_attend_many(const AttentionPlan &p, hipStream_t st) {
+    return p.a.dtype == CBS_DTYPE_BF16 ? launch1<__bf16>(p, st) : launch1<_Float16>(p, st);
+}
+
+}  // namespace cbs
