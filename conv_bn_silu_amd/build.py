@@ -1,6 +1,7 @@
-"""Compile the HIP library ``libconv_bn_silu.so`` for gfx950 (in-tree).
+"""Compile the HIP library ``libconv_bn_silu.so`` for gfx950 and the Python
+module ``_block8.so`` that calls it (both in-tree).
 
-Every ``csrc/*.hip`` and ``csrc/*.cpp`` is compiled by hipcc to its own object
+Every ``csrc/*.hip`` and ``csrc/*.cpp`` but ``py_*.cpp`` is compiled by hipcc to its own object
 (in parallel) and linked into one shared library next to this file.  All HIP
 code is compiled without packed-fp32 instructions.
 
@@ -18,12 +19,14 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconv_bn_silu.so")
 RESOURCES = os.path.join(HERE, "libconv_bn_silu.resources.txt")
+MODULE = os.path.join(HERE, "_block8.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -32,7 +35,8 @@ COMMON = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "*.cpp")))
+    cpp = [s for s in glob.glob(os.path.join(CSRC, "*.cpp")) if not os.path.basename(s).startswith("py_")]
+    return sorted(glob.glob(os.path.join(CSRC, "*.hip")) + cpp)
 
 
 _REMARK = re.compile(r"remark:\s+(Function Name|VGPRs|AGPRs|ScratchSize \[bytes/lane\]|Occupancy \[waves/SIMD\]|"
@@ -70,6 +74,22 @@ def _compile(src: str, extra: list[str]) -> tuple[str, list[dict]]:
     return obj, parse_resources(res.stderr)
 
 
+def build_module() -> str:
+    """The Python module: host code only, against PyTorch's headers and the library."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = MODULE + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include/torch/csrc/api/include"),
+           "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "py_block8.cpp"), "-o", tmp, "-L" + HERE, "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(root, "lib"),
+           "-l:libconv_bn_silu.so", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, MODULE)
+    return MODULE
+
+
 def build(extra: list[str] | None = None, jobs: int = 8) -> str:
     """Compile and link; returns the path of the shared library."""
     os.makedirs(BUILD, exist_ok=True)
@@ -90,6 +110,7 @@ def build(extra: list[str] | None = None, jobs: int = 8) -> str:
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    build_module()
     return LIB
 
 

@@ -98,11 +98,6 @@ __device__ __forceinline__ int64_t few_line(const AttentionPlan &p, const Sequen
     return p.few_only ? out_line(p, s, kvh, r) : ((int64_t)s.b * p.a.cache.heads + kvh) * p.few.tile + r;
 }
 
-// 16 bytes at any address, as one load.
-struct __attribute__((packed, aligned(1))) Any16 {
-    u32x4 v;
-};
-
 // 4 codes as fp16: with the sign bit flipped, the byte below 0x64 is the fp16
 // number 1024 + 128 + code.
 __device__ __forceinline__ f16x4 codes_f16(uint32_t c) {

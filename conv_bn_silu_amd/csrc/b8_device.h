@@ -16,40 +16,35 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
-// Value types of the operators' inputs and outputs, 8 elements at a time.
-// `load8` needs 16-byte alignment; `load1` is for tensors without it and for
-// ragged ends.  Stores round to nearest even.
-template <typename T> struct Value;
+// 16 bytes at any address: the memory path serves them as one access whatever the
+// alignment, so that one kernel does for tensors at multiples of 16 bytes and others.
+struct __attribute__((packed, aligned(1))) Any16 {
+    u32x4 v;
+};
+
+// Value types of the operators' inputs and outputs, 8 elements at a time or one (for
+// ragged ends).  Stores round to nearest even.
+template <typename T> struct Value {
+    typedef T x8 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ float load1(const T *p) { return (float)*p; }
+    static __device__ __forceinline__ void store1(T *p, float v) { *p = (T)v; }
+    static __device__ __forceinline__ f32x8 load8(const T *p) {
+        return __builtin_convertvector(__builtin_bit_cast(x8, ((const Any16 *)p)->v), f32x8);
+    }
+    static __device__ __forceinline__ void store8(T *p, f32x8 v) {
+        ((Any16 *)p)->v = __builtin_bit_cast(u32x4, __builtin_convertvector(v, x8));
+    }
+};
 template <> struct Value<float> {
     static __device__ __forceinline__ float load1(const float *p) { return *p; }
     static __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
     static __device__ __forceinline__ f32x8 load8(const float *p) {
-        const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+        const f32x4 a = __builtin_bit_cast(f32x4, ((const Any16 *)p)[0].v), b = __builtin_bit_cast(f32x4, ((const Any16 *)p)[1].v);
         return f32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     }
     static __device__ __forceinline__ void store8(float *p, f32x8 v) {
-        *(f32x4 *)p = f32x4{v[0], v[1], v[2], v[3]};
-        *(f32x4 *)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    }
-};
-template <> struct Value<__bf16> {
-    static __device__ __forceinline__ float load1(const __bf16 *p) { return (float)*p; }
-    static __device__ __forceinline__ void store1(__bf16 *p, float v) { *p = (__bf16)v; }
-    static __device__ __forceinline__ f32x8 load8(const __bf16 *p) {
-        return __builtin_convertvector(*(const bf16x8 *)p, f32x8);
-    }
-    static __device__ __forceinline__ void store8(__bf16 *p, f32x8 v) {
-        *(bf16x8 *)p = __builtin_convertvector(v, bf16x8);
-    }
-};
-template <> struct Value<_Float16> {
-    static __device__ __forceinline__ float load1(const _Float16 *p) { return (float)*p; }
-    static __device__ __forceinline__ void store1(_Float16 *p, float v) { *p = (_Float16)v; }
-    static __device__ __forceinline__ f32x8 load8(const _Float16 *p) {
-        return __builtin_convertvector(*(const f16x8 *)p, f32x8);
-    }
-    static __device__ __forceinline__ void store8(_Float16 *p, f32x8 v) {
-        *(f16x8 *)p = __builtin_convertvector(v, f16x8);
+        ((Any16 *)p)[0].v = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+        ((Any16 *)p)[1].v = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
     }
 };
 

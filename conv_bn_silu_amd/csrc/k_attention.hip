@@ -11,24 +11,54 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One row: its chunks' parts, brought to one maximum and added.  A wave to a row.
-template <typename T>
-__device__ __forceinline__ void join(const AttentionPlan &p, const AttentionPart &part, int64_t line, int n, int64_t out) {
+// One row: its chunks' parts, brought to one maximum and added.  A wave to a row: its
+// lanes are the chunks where maxima and sums are concerned, and the dims for the outputs,
+// whose loads for 8 chunks at a time do not wait for each other.
+template <typename T, int ND>
+__device__ __forceinline__ void join_dims(const AttentionPlan &p, const AttentionPart &part, int64_t line, int n, int64_t out) {
     const int lane = (int)threadIdx.x % 64, dim = p.a.cache.dim;
     const float *ml = part.ml + 2 * line * part.chunks, *o = part.o + line * part.chunks * dim;
     float top = -INFINITY;
-    for (int c = 0; c < n; ++c) top = fmaxf(top, ml[2 * c]);
-    float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int c = 0; c < n; ++c) {
-        const float f = ml[2 * c] == top ? 1.f : __builtin_amdgcn_exp2f(ml[2 * c] - top);
-        sum += ml[2 * c + 1] * f;
+    for (int c = lane; c < n; c += 64) top = fmaxf(top, ml[2 * c]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (64 * i + lane < dim) v[i] += o[(int64_t)c * dim + 64 * i + lane] * f;
+    for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x, 64));
+    float sum = 0.f, v[ND] = {};
+    for (int c0 = 0; c0 < n; c0 += 64) {
+        float f = 0.f, l = 0.f;
+        if (c0 + lane < n) {
+            const float m = ml[2 * (c0 + lane)];
+            f = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top);
+            l = ml[2 * (c0 + lane) + 1] * f;
+        }
+#pragma unroll
+        for (int x = 1; x < 64; x *= 2) l += __shfl_xor(l, x, 64);
+        sum += l;
+        const int n0 = min(64, n - c0);
+        for (int c = 0; c < n0; c += 8) {
+            float part_o[8][ND];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int i = 0; i < ND; ++i)
+                    part_o[e][i] = o[(int64_t)(c0 + min(c + e, n0 - 1)) * dim + min(64 * i + lane, dim - 1)];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float w = __shfl(f, min(c + e, 63), 64);
+#pragma unroll
+                for (int i = 0; i < ND; ++i)
+                    if (c + e < n0) v[i] += part_o[e][i] * w;
+            }
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < ND; ++i)
         if (64 * i + lane < dim) Value<T>::store1((T *)p.a.out + out * dim + 64 * i + lane, divide(v[i], sum));
+}
+
+template <typename T>
+__device__ __forceinline__ void join(const AttentionPlan &p, const AttentionPart &part, int64_t line, int n, int64_t out) {
+    if (p.a.cache.dim <= 128) join_dims<T, 2>(p, part, line, n, out);
+    else join_dims<T, 4>(p, part, line, n, out);
 }
 
 // A workgroup to a sequence and key/value head.

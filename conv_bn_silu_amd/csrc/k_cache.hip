@@ -38,28 +38,9 @@ __device__ __forceinline__ int64_t cache_row(const CacheParams &p, uint32_t slot
     return ((int64_t)page * p.io.cache.heads + head) * p.page.d + off;
 }
 
-template <typename T, bool VEC> __device__ __forceinline__ f32x8 load8_or_1(const T *p) {
-    if constexpr (VEC) {
-        return Value<T>::load8(p);
-    } else {
-        f32x8 x;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = Value<T>::load1(p + i);
-        return x;
-    }
-}
-template <typename T, bool VEC> __device__ __forceinline__ void store8_or_1(T *p, f32x8 x) {
-    if constexpr (VEC) {
-        Value<T>::store8(p, x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) Value<T>::store1(p + i, x[i]);
-    }
-}
-
 // T: type of the values given; C: the cache's (int8_t, or a value type).
 // blockIdx.y: 0 keys, 1 values.
-template <typename T, typename C, int TEAM, bool VEC>
+template <typename T, typename C, int TEAM>
 __global__ __launch_bounds__(kThreads) void cache_write(const CacheParams p) {
     const uint32_t row = blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM;
     const int d = (int)(threadIdx.x % TEAM) * 8, dim = p.io.cache.dim;
@@ -72,7 +53,7 @@ __global__ __launch_bounds__(kThreads) void cache_write(const CacheParams p) {
                    head * (second ? p.io.v_head : p.io.k_head);
     const bool mine = d < dim;
     f32x8 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (mine) x = load8_or_1<T, VEC>(src + d);
+    if (mine) x = Value<T>::load8(src + d);
     const int64_t at = cache_row(p, slot, head);
     C *dst = (C *)(second ? p.io.cache.v : p.io.cache.k) + at * dim + d;
     if constexpr (std::is_same_v<C, int8_t>) {
@@ -90,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void cache_write(const CacheParams p) {
     }
 }
 
-template <typename T, typename C, int TEAM, bool VEC>
+template <typename T, typename C, int TEAM>
 __global__ __launch_bounds__(kThreads) void cache_read(const CacheParams p) {
     const uint32_t row = blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM;
     const int d = (int)(threadIdx.x % TEAM) * 8, dim = p.io.cache.dim;
@@ -111,7 +92,7 @@ __global__ __launch_bounds__(kThreads) void cache_read(const CacheParams p) {
             x = Value<C>::load8(src);
         }
     }
-    store8_or_1<T, VEC>((T *)(second ? p.io.v_out : p.io.k_out) + (int64_t)row * dim + d, x);
+    Value<T>::store8((T *)(second ? p.io.v_out : p.io.k_out) + (int64_t)row * dim + d, x);
 }
 
 CacheParams params(const CacheIo &a) {
@@ -119,42 +100,29 @@ CacheParams params(const CacheIo &a) {
                        (uint32_t)(a.tokens * a.cache.heads), (uint32_t)(a.cache.pages * a.cache.page_size)};
 }
 
-template <typename T, typename C, int TEAM> hipError_t launch3(const CacheIo &a, bool write, bool vec, hipStream_t st) {
+template <typename T, typename C, int TEAM> hipError_t launch3(const CacheIo &a, bool write, hipStream_t st) {
     const CacheParams p = params(a);
     const dim3 grid((p.rows + kThreads / TEAM - 1) / (kThreads / TEAM), 2);
-    if (write) {
-        if (vec) cache_write<T, C, TEAM, true><<<grid, kThreads, 0, st>>>(p);
-        else cache_write<T, C, TEAM, false><<<grid, kThreads, 0, st>>>(p);
-    } else {
-        if (vec) cache_read<T, C, TEAM, true><<<grid, kThreads, 0, st>>>(p);
-        else cache_read<T, C, TEAM, false><<<grid, kThreads, 0, st>>>(p);
-    }
+    if (write) cache_write<T, C, TEAM><<<grid, kThreads, 0, st>>>(p);
+    else cache_read<T, C, TEAM><<<grid, kThreads, 0, st>>>(p);
     return hipGetLastError();
 }
-template <typename T, typename C> hipError_t launch2(const CacheIo &a, bool write, bool vec, hipStream_t st) {
-    return a.cache.dim <= 128 ? launch3<T, C, 16>(a, write, vec, st) : launch3<T, C, 32>(a, write, vec, st);
+template <typename T, typename C> hipError_t launch2(const CacheIo &a, bool write, hipStream_t st) {
+    return a.cache.dim <= 128 ? launch3<T, C, 16>(a, write, st) : launch3<T, C, 32>(a, write, st);
 }
-template <typename T> hipError_t launch1(const CacheIo &a, bool write, bool vec, hipStream_t st) {
+template <typename T> hipError_t launch1(const CacheIo &a, bool write, hipStream_t st) {
     switch (a.cache.dtype) {
-        case CBS_DTYPE_I8: return launch2<T, int8_t>(a, write, vec, st);
-        case CBS_DTYPE_F32: return launch2<T, float>(a, write, vec, st);
-        case CBS_DTYPE_BF16: return launch2<T, __bf16>(a, write, vec, st);
-        default: return launch2<T, _Float16>(a, write, vec, st);
+        case CBS_DTYPE_I8: return launch2<T, int8_t>(a, write, st);
+        case CBS_DTYPE_F32: return launch2<T, float>(a, write, st);
+        case CBS_DTYPE_BF16: return launch2<T, __bf16>(a, write, st);
+        default: return launch2<T, _Float16>(a, write, st);
     }
 }
 hipError_t launch(const CacheIo &a, bool write, hipStream_t st) {
-    // vector accesses need every row to start at a multiple of 16 bytes
-    const int64_t e = a.dtype == CBS_DTYPE_F32 ? 4 : 2;
-    bool vec;
-    if (write)
-        vec = ((uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)(e * a.k_token) | (uintptr_t)(e * a.k_head) |
-               (uintptr_t)(e * a.v_token) | (uintptr_t)(e * a.v_head)) % 16 == 0;
-    else
-        vec = ((uintptr_t)a.k_out | (uintptr_t)a.v_out) % 16 == 0;  // dim is a multiple of 8
     switch (a.dtype) {
-        case CBS_DTYPE_F32: return launch1<float>(a, write, vec, st);
-        case CBS_DTYPE_BF16: return launch1<__bf16>(a, write, vec, st);
-        default: return launch1<_Float16>(a, write, vec, st);
+        case CBS_DTYPE_F32: return launch1<float>(a, write, st);
+        case CBS_DTYPE_BF16: return launch1<__bf16>(a, write, st);
+        default: return launch1<_Float16>(a, write, st);
     }
 }
 

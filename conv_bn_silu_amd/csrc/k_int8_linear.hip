@@ -15,15 +15,10 @@
 namespace cbs {
 namespace {
 
-// 16 bytes at any address, as one load.
-struct __attribute__((packed, aligned(1))) Bytes16 {
-    i32x4 v;
-};
-
 // 16 bytes of w at byte `at`, some or all of which may lie past its `size` bytes: those
 // come as zero and are not read.
 __device__ __forceinline__ i32x4 load_end(const int8_t *w, int64_t at, int64_t size) {
-    if (at + 16 <= size) return ((const Bytes16 *)(w + at))->v;
+    if (at + 16 <= size) return __builtin_bit_cast(i32x4, ((const Any16 *)(w + at))->v);
     uint64_t lo = 0, hi = 0;
 #pragma unroll 1
     for (int64_t i = size - 1; i >= at; --i) {
@@ -92,7 +87,7 @@ __global__ __launch_bounds__(kStreamThreads) void linear_stream(const StreamPara
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int8_t *at = wr[j] + s * 128 + h * 64;
-                f[j][h] = s < full ? ((const Bytes16 *)at)->v : load_end(p.w, at - p.w, size);
+                f[j][h] = s < full ? __builtin_bit_cast(i32x4, ((const Any16 *)at)->v) : load_end(p.w, at - p.w, size);
             }
     };
     auto load_a = [&](int s, i32x4(&f)[MT][2]) {
@@ -110,9 +105,8 @@ __global__ __launch_bounds__(kStreamThreads) void linear_stream(const StreamPara
         constexpr int kTeam = kStreamThreads / ROWS;  // lanes to a row
         const int m = (int)threadIdx.x / kTeam, t = (int)threadIdx.x % kTeam;
         const T *x = (const T *)p.x + (int64_t)min(m, p.M - 1) * p.x_stride;
-        const bool vec = ((uintptr_t)p.x | (uintptr_t)(p.x_stride * (int64_t)sizeof(T))) % 16 == 0;
         auto chunk = [&](int k) {
-            if (vec && k + 8 <= p.K) return Value<T>::load8(x + k);
+            if (k + 8 <= p.K) return Value<T>::load8(x + k);
             f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -222,7 +216,6 @@ struct TileParams {
     const float *w_scale, *bias;
     void *y;
     int M, N, m_tiles, n_tiles;
-    bool y_vec;  // rows of y start at multiples of 16 bytes
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -346,7 +339,7 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64), 2) void linear_t
             for (int e = 0; e < 8; ++e)
                 v[e] = linear_epilogue<T, SILU>(e < 4 ? lo[e % 4] : hi[e % 4], sa, sw[e], bias[e]);
             T *to = (T *)p.y + (int64_t)m * p.N + n;
-            if (p.y_vec && n + 8 <= p.N) {
+            if (n + 8 <= p.N) {
                 Value<T>::store8(to, v);
             } else {
 #pragma unroll
@@ -414,8 +407,7 @@ template <typename T, bool SILU> hipError_t launch2(const LinearArgs &a, const C
     if (kind == kStream || (!copy && (uintptr_t)a.w % 16 != 0)) return launch_stream<T>(a, l, st);
     hipError_t e = launch_quant_rows(a, l, st);
     if (e != hipSuccess) return e;
-    TileParams p{l, a.w, a.K, a.w_scale, a.bias, a.y, a.M, a.N, 0, 0, false};
-    p.y_vec = (uintptr_t)a.y % 16 == 0 && (int64_t)a.N * (int64_t)sizeof(T) % 16 == 0;
+    TileParams p{l, a.w, a.K, a.w_scale, a.bias, a.y, a.M, a.N, 0, 0};
     if (copy) {
         int8_t *to = l.codes + (int64_t)l.rows * l.Kp;
         align_rows<<<(unsigned)(((int64_t)a.N * (l.Kp / 16) + 255) / 256), 256, 0, st>>>(a.w, to, a.N, a.K, l.Kp);

@@ -20,9 +20,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunks = 4;  // of 8 values a lane keeps
 
-template <typename T, bool VEC> __device__ __forceinline__ f32x8 load_chunk(const T *row, int k, int K) {
+template <typename T> __device__ __forceinline__ f32x8 load_chunk(const T *row, int k, int K) {
     f32x8 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (VEC && k + 8 <= K) return Value<T>::load8(row + k);
+    if (k + 8 <= K) return Value<T>::load8(row + k);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (k + i < K) x[i] = Value<T>::load1(row + k + i);
@@ -42,7 +42,7 @@ __device__ __forceinline__ void store_chunk(int8_t *codes, int rows, int m, int 
 }
 
 // TEAM lanes per row: 64 or 256.
-template <typename T, bool VEC, int TEAM>
+template <typename T, int TEAM>
 __global__ __launch_bounds__(kThreads) void quant_rows(const T *__restrict__ x, int64_t x_stride, int M, int K, int Kp,
                                                        int rows, int8_t *__restrict__ codes,
                                                        float *__restrict__ scales) {
@@ -56,10 +56,10 @@ __global__ __launch_bounds__(kThreads) void quant_rows(const T *__restrict__ x, 
     uint32_t top = 0;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        keep[c] = load_chunk<T, VEC>(row, (c * TEAM + lane) * 8, K);
+        keep[c] = load_chunk<T>(row, (c * TEAM + lane) * 8, K);
         top = max(top, chunk_max(keep[c]));
     }
-    for (int k = kSpan + lane * 8; k < K; k += TEAM * 8) top = max(top, chunk_max(load_chunk<T, VEC>(row, k, K)));
+    for (int k = kSpan + lane * 8; k < K; k += TEAM * 8) top = max(top, chunk_max(load_chunk<T>(row, k, K)));
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
     if constexpr (TEAM == 256) {
@@ -74,21 +74,17 @@ __global__ __launch_bounds__(kThreads) void quant_rows(const T *__restrict__ x, 
         if (k < Kp) store_chunk(codes, rows, m, k, keep[c], s, inv);
     }
     for (int k = kSpan + lane * 8; k < Kp; k += TEAM * 8)
-        store_chunk(codes, rows, m, k, load_chunk<T, VEC>(row, k, K), s, inv);
+        store_chunk(codes, rows, m, k, load_chunk<T>(row, k, K), s, inv);
     if (lane == 0) scales[m] = s;
 }
 
-template <typename T, bool VEC> hipError_t launch2(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
+template <typename T> hipError_t launch1(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
     const T *x = (const T *)a.x;
     if (a.K <= 2048)
-        quant_rows<T, VEC, 64><<<(a.M + 3) / 4, kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes, l.scales);
+        quant_rows<T, 64><<<(a.M + 3) / 4, kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes, l.scales);
     else
-        quant_rows<T, VEC, 256><<<a.M, kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes, l.scales);
+        quant_rows<T, 256><<<a.M, kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes, l.scales);
     return hipGetLastError();
-}
-template <typename T> hipError_t launch1(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
-    const bool vec = ((uintptr_t)a.x | (uintptr_t)(a.x_stride * (int64_t)sizeof(T))) % 16 == 0;
-    return vec ? launch2<T, true>(a, l, st) : launch2<T, false>(a, l, st);
 }
 
 }  // namespace

@@ -45,8 +45,7 @@ enum { CBS_ACT_NONE = 0, CBS_ACT_SILU = 1 };
  * M = 0 is a no-op.  1 <= K <= 131072 (the sum then fits 32 bits), 1 <= N,
  * and M, N <= 2^24, else CBS_ERR_INVALID_ARG (sizes below 1) or
  * CBS_ERR_UNSUPPORTED.  y and the workspace must not overlap an input or
- * each other.  Any alignment to the element size is served; rows and pointers
- * at multiples of 16 bytes take the vectorised kernels. */
+ * each other.  Any alignment to the element size is served. */
 int cbs_int8_linear(conv_bn_silu_t handle, const void *x, int64_t x_stride, const int8_t *w, const float *w_scale,
                     const float *bias, void *y, int64_t M, int64_t N, int64_t K, int dtype, int activation,
                     void *workspace, int64_t workspace_bytes, void *stream);
