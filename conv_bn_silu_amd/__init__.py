@@ -21,9 +21,12 @@ __all__ = ["conv_bn_silu", "conv_bn_silu_unfused", "fold_bn", *_BLOCK8, "binding
 
 def __getattr__(name):
     if name in ("binding", "block8", "synth"):
-        return importlib.import_module(f"{__name__}.{name}")
-    if name in ("conv_bn_silu", "conv_bn_silu_unfused", "fold_bn", "Library"):
-        return getattr(importlib.import_module(f"{__name__}.binding"), name)
-    if name in _BLOCK8:
-        return getattr(importlib.import_module(f"{__name__}.block8"), name)
-    raise AttributeError(name)
+        value = importlib.import_module(f"{__name__}.{name}")
+    elif name in ("conv_bn_silu", "conv_bn_silu_unfused", "fold_bn", "Library"):
+        value = getattr(importlib.import_module(f"{__name__}.binding"), name)
+    elif name in _BLOCK8:
+        value = getattr(importlib.import_module(f"{__name__}.block8"), name)
+    else:
+        raise AttributeError(name)
+    globals()[name] = value  # found once: looking it up here again took 7 us an import
+    return value
