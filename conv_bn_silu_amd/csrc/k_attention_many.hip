@@ -100,7 +100,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     __shared__ __attribute__((aligned(16))) float kscale[2][KT], vscale[2][KT];
     __shared__ uint64_t valid_bits[2];
     __shared__ float vrefs[2];
-    __shared__ int bad[2][8];
+    __shared__ int taken_out[2];  // the last step in whose values store() found something to take out
     const AttentionArgs &a = p.a;
     const int tid = (int)threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int col = lane % 32, half = lane / 32;
@@ -129,7 +129,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     // this lane's row
     const int r = min(r0 + 32 * wave + col, r1 - 1), tok = (int)p.group.div((uint32_t)r);
     const int pos = old + tok, low = first_key(p, pos);
-    float qf = fabsf(a.scale) * kLog2e;
+    float qf = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-149f);  // above zero, so that -inf stays what it is
     X8 q[kSteps];
     {
         const T *src = (const T *)a.q + (int64_t)(seq.first + tok) * a.q_token +
@@ -153,7 +153,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                 for (int e = 0; e < 4; ++e) top = max(top, max(raw[s][e] & 0x7FFFu, (raw[s][e] >> 16) & 0x7FFFu));
             top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
             const int e = top >= 0x7F80u ? 0 : min(126, 141 - (int)(top >> 7));
-            qf = __builtin_ldexpf(qf, -e);
+            qf = fmaxf(__builtin_ldexpf(qf, -e), 0x1p-149f);
             const float up = __builtin_ldexpf(1.f, e);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
@@ -203,8 +203,8 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
         }
     };
     // Values that only some of the tile's rows see may be infinite or NaN, and zero times
-    // those is no zero: where the step is one that some rows see in part, they are
-    // taken out here and added apart.
+    // those is no zero: where some rows see a step in part, they are taken out here and
+    // added apart.  8-bit codes are finite; their scales are taken out wherever they are not.
     const int tile_min = old + (int)p.group.div((uint32_t)r0);
     const int tile_low = first_key(p, old + (int)p.group.div((uint32_t)(r1 - 1)));
     auto store = [&](int buf, int j0) {
@@ -236,14 +236,16 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
             }
         }
         if constexpr (!S::kI8) {
-            const bool any = __any(odd);
-            if (lane == 0) bad[buf][wave] = any ? 1 : 0;
+            if (__any(odd) && lane == 0) taken_out[buf] = j0;
         }
         if (wave == 0) {
             if constexpr (S::kI8) {
                 const uint32_t bits = magnitude(vs);
-                const bool counts = ((key_bits >> lane) & 1) && bits < 0x7F800000u;
-                if (__any(counts && vs > vref)) {
+                const bool there = (key_bits >> lane) & 1, counts = there && bits < 0x7F800000u;
+                const uint64_t taken = __ballot(there && !counts);
+                if (taken && lane == 0) taken_out[buf] = j0;
+                if (!counts) vs = 0.f;
+                if (__any(vs > vref)) {
                     uint32_t top = counts ? bits : 0u;
 #pragma unroll
                     for (int x = 1; x < 64; x *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, x, 64));
@@ -257,9 +259,15 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
         }
     };
 
+    // where the lane's reads of a buffer's keys and values begin
+    const int k_lane = col * S::kPitch + ((half ^ S::swap_k(col)) * 16), v_row = 4 * half + lane % 16 / 4;
+    const int v_lane = v_row * S::kPitch + (((2 * (lane / 16 % 2) + lane % 4 / 2) ^ S::swap_v(v_row)) * 16) + lane % 2 * 8;
+
     f32x16 o[NB] = {};
     float m = -INFINITY, l = 0.f, o_ref = 0x1p-126f;
 
+    if (tid < 2) taken_out[tid] = -1;
+    __syncthreads();
     if (lo < hi) {
         look_up(lo);
         load(lo);
@@ -275,21 +283,20 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
             if (j0 + 2 * KT < hi) look_up(j0 + 2 * KT);
         }
         if (j0 <= wave_max && j0 + KT > wave_low) {
-            const unsigned char *const kbuf = lds + buf * 2 * S::kSide, *const vbuf = kbuf + S::kSide;
-            // LDS addresses are made anew for each step: kept, they cost a register for each access
-            int my = lane;
-            asm volatile("" : "+v"(my));
-            const int my_col = my % 32, my_half = my / 32;
-            f32x16 s[2] = {};
+            // An operand's piece number is exchanged by exclusive or, and so is its byte: one
+            // operation for a step of the scores or a block of the outputs, and the rest is
+            // the instruction's offset.
+            int k_at = buf * 2 * S::kSide + k_lane, v_at = buf * 2 * S::kSide + S::kSide + v_lane;
+            asm volatile("" : "+v"(k_at), "+v"(v_at));  // made anew for each step, or each costs a register
+            f32x16 s[2];
 #pragma unroll
             for (int st = 0; st < kSteps; ++st)
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
-                    const X8 kf = *(const X8 *)(kbuf + (32 * kb + my_col) * S::kPitch + (((2 * st + my_half) ^ S::swap_k(my_col)) * 16));
-                    s[kb] = mma32(kf, q[st], s[kb]);
+                    const X8 kf = *(const X8 *)(lds + (k_at ^ (32 * st)) + 32 * kb * S::kPitch);
+                    s[kb] = mma32(kf, q[st], st ? s[kb] : f32x16{});
                 }
             const uint64_t valid = valid_bits[buf];
-            const bool full = valid == ~0ull && j0 + KT - 1 <= wave_min && j0 >= wave_high_low;
             // the lane's keys are 32 kb + 8 g + 4 half + 0..3
             if constexpr (S::kI8) {
 #pragma unroll
@@ -301,17 +308,15 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                         for (int e = 0; e < 4; ++e) s[kb][4 * g + e] *= k4[e];
                     }
             }
-            uint32_t seen = ~0u;
-            if (!full) {
-                seen = 0;
+            if (!(valid == ~0ull && j0 + KT - 1 <= wave_min && j0 >= wave_high_low)) {
+                int my_half = half;
+                asm volatile("" : "+v"(my_half));
                 const uint64_t ahead = valid >> (4 * my_half);
                 const int last = pos - j0 - 4 * my_half, first = low - j0 - 4 * my_half;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int key = 32 * (i / 16) + 8 * (i % 16 / 4) + i % 4;  // less 4 half
-                    const bool see = ((ahead >> key) & 1) && key <= last && key >= first;
-                    seen |= see ? 1u << i : 0u;
-                    if (!see) s[i / 16][i % 16] = -INFINITY;
+                    if (!(((ahead >> key) & 1) && key <= last && key >= first)) s[i / 16][i % 16] = -INFINITY;
                 }
             }
             float tops[4];
@@ -338,6 +343,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
 #pragma unroll
                 for (int db = 0; db < NB; ++db) o[db] *= both;
             }
+            // a key that is not seen: 2^-inf = 0
             const float base = m == -INFINITY ? 0.f : m * qf;
             X8 pr[4];
             float sums[4] = {0.f, 0.f, 0.f, 0.f};
@@ -349,54 +355,46 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                     if constexpr (S::kI8) v4 = *(const f32x4 *)(&vscale[buf][32 * kb + 8 * g + 4 * half]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const bool hide = !full && !((seen >> (16 * kb + 4 * g + e)) & 1);
                         float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][4 * g + e], qf, -base));
-                        if (hide) w = 0.f;
                         sums[e] += w;
-                        if constexpr (S::kI8) {
-                            w *= v4[e];
-                            if (hide) w = 0.f;  // the scale may be anything
-                        }
+                        if constexpr (S::kI8) w *= v4[e];
                         pr[2 * kb + g / 2][g % 2 * 4 + e] = (X)w;
                     }
                 }
             l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
 
             // values: keys 16 t + 4 half + 0..3 and 8 above those, of dim 32 db + col
-            auto values = [&](int db, int t) {
-                const int row = 16 * t + 4 * my_half + my % 16 / 4, piece = 4 * db + 2 * (my / 16 % 2) + my % 4 / 2;
-                const unsigned char *from = vbuf + row * S::kPitch + ((piece ^ S::swap_v(row)) * 16) + my % 2 * 8;
-                const u32x2 x = read_tr16(from), y = read_tr16(from + 8 * S::kPitch);
-                return u32x4{x.x, x.y, y.x, y.y};
-            };
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int db = 0; db < NB; ++db) o[db] = mma32(__builtin_bit_cast(X8, values(db, t)), pr[t], o[db]);
-            if constexpr (!S::kI8) {
-                int odd = 0;
-#pragma unroll
-                for (int w = 0; w < S::kWaves; ++w) odd |= bad[buf][w];
-                if (odd) {
-                    // the values that store() has taken out, to the rows that see them
+                for (int db = 0; db < NB; ++db) {
+                    const unsigned char *from = lds + (v_at ^ (64 * db)) + 16 * t * S::kPitch;
+                    const u32x2 x = read_tr16(from), y = read_tr16(from + 8 * S::kPitch);
+                    o[db] = mma32(__builtin_bit_cast(X8, u32x4{x.x, x.y, y.x, y.y}), pr[t], o[db]);
+                }
+            if (__builtin_expect(taken_out[buf] == j0, 0)) {
+                // what store() has taken out, to the rows that see it
 #pragma unroll 1
-                    for (int j = j0; j < min(hi, j0 + KT); ++j) {
-                        bool there;
-                        const int64_t row = row_of(j, table[p.page.div((uint32_t)j)], there);
-                        const bool sees = there && j <= pos && j >= low;
-#pragma unroll
-                        for (int db = 0; db < NB; ++db)
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const int d = 32 * db + 8 * g + 4 * half;
-                                if (d >= dim || !sees) continue;
-                                typedef X x4 __attribute__((ext_vector_type(4)));
-                                const x4 v = *(const x4 *)((const X *)vdata + row * dim + d);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (!__builtin_isfinite((float)v[e])) o[db][4 * g + e] += (float)v[e];
-                            }
+                for (int j = j0; j < min(hi, j0 + KT); ++j) {
+                    bool there;
+                    const int64_t row = row_of(j, table[p.page.div((uint32_t)j)], there);
+                    const bool sees = there && j <= pos && j >= low;
+                    if constexpr (S::kI8) {
+                        if (__builtin_isfinite(a.cache.v_scale[row])) continue;
                     }
+#pragma unroll
+                    for (int db = 0; db < NB; ++db)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int d = 32 * db + 8 * g + 4 * half;
+                            if (d >= dim || !sees) continue;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float v = (float)vdata[row * dim + d + e];
+                                if constexpr (S::kI8) v *= a.cache.v_scale[row];
+                                if (!__builtin_isfinite(v)) o[db][4 * g + e] += v;
+                            }
+                        }
                 }
             }
         }
