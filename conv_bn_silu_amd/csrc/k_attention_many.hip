@@ -95,7 +95,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     using S = ManyShape<C, NB>;
     using X8 = typename Operand<T, C>::x8;
     using X = typename Operand<T, C>::type;
-    constexpr int kSteps = 2 * NB;
+    constexpr int kSteps = 2 * NB, kAhead = 4;
     __shared__ __attribute__((aligned(16))) unsigned char lds[S::kBytes];
     __shared__ __attribute__((aligned(16))) float kscale[2][KT], vscale[2][KT];
     __shared__ uint64_t valid_bits[2];
@@ -288,25 +288,28 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
             // the instruction's offset.
             int k_at = buf * 2 * S::kSide + k_lane, v_at = buf * 2 * S::kSide + S::kSide + v_lane;
             asm volatile("" : "+v"(k_at), "+v"(v_at));  // made anew for each step, or each costs a register
+            // Fragments are read kAhead matrix instructions before their use, and the order is
+            // held: left alone the compiler reads each just before it is wanted, and waits.
+            auto read_k = [&](int i) { return *(const X8 *)(lds + (k_at ^ (32 * (i / 2))) + 32 * (i % 2) * S::kPitch); };
             f32x16 s[2];
+            X8 ring[kAhead];
 #pragma unroll
-            for (int st = 0; st < kSteps; ++st)
+            for (int i = 0; i < kAhead; ++i) ring[i] = read_k(i);
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    const X8 kf = *(const X8 *)(lds + (k_at ^ (32 * st)) + 32 * kb * S::kPitch);
-                    s[kb] = mma32(kf, q[st], st ? s[kb] : f32x16{});
-                }
+            for (int i = 0; i < 2 * kSteps; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                s[i % 2] = mma32(ring[i % kAhead], q[i / 2], i < 2 ? f32x16{} : s[i % 2]);
+                if (i + kAhead < 2 * kSteps) ring[i % kAhead] = read_k(i + kAhead);
+            }
             const uint64_t valid = valid_bits[buf];
             // the lane's keys are 32 kb + 8 g + 4 half + 0..3
+            f32x4 per_key[8];
             if constexpr (S::kI8) {
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+                for (int g = 0; g < 8; ++g) per_key[g] = *(const f32x4 *)(&kscale[buf][8 * g + 4 * half]);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const f32x4 k4 = *(const f32x4 *)(&kscale[buf][32 * kb + 8 * g + 4 * half]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[kb][4 * g + e] *= k4[e];
-                    }
+                for (int i = 0; i < 32; ++i) s[i / 16][i % 16] *= per_key[i / 4][i % 4];
             }
             if (!(valid == ~0ull && j0 + KT - 1 <= wave_min && j0 >= wave_high_low)) {
                 int my_half = half;
@@ -343,35 +346,37 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
 #pragma unroll
                 for (int db = 0; db < NB; ++db) o[db] *= both;
             }
+            if constexpr (S::kI8) {
+#pragma unroll
+                for (int g = 0; g < 8; ++g) per_key[g] = *(const f32x4 *)(&vscale[buf][8 * g + 4 * half]);
+            }
+            // values: keys 16 t + 4 half + 0..3 and 8 above those, of dim 32 db + col
+            auto read_v = [&](int i) {
+                const unsigned char *from = lds + (v_at ^ (64 * (i % NB))) + 16 * (i / NB) * S::kPitch;
+                const u32x2 x = read_tr16(from), y = read_tr16(from + 8 * S::kPitch);
+                return __builtin_bit_cast(X8, u32x4{x.x, x.y, y.x, y.y});
+            };
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) ring[i] = read_v(i);
+            __builtin_amdgcn_sched_barrier(0);
             // a key that is not seen: 2^-inf = 0
             const float base = m == -INFINITY ? 0.f : m * qf;
             X8 pr[4];
             float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    f32x4 v4;
-                    if constexpr (S::kI8) v4 = *(const f32x4 *)(&vscale[buf][32 * kb + 8 * g + 4 * half]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][4 * g + e], qf, -base));
-                        sums[e] += w;
-                        if constexpr (S::kI8) w *= v4[e];
-                        pr[2 * kb + g / 2][g % 2 * 4 + e] = (X)w;
-                    }
-                }
+            for (int i = 0; i < 32; ++i) {
+                float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 16][i % 16], qf, -base));
+                sums[i % 4] += w;
+                if constexpr (S::kI8) w *= per_key[i / 4][i % 4];
+                pr[i / 8][i % 8] = (X)w;
+            }
             l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
-
-            // values: keys 16 t + 4 half + 0..3 and 8 above those, of dim 32 db + col
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int db = 0; db < NB; ++db) {
-                    const unsigned char *from = lds + (v_at ^ (64 * db)) + 16 * t * S::kPitch;
-                    const u32x2 x = read_tr16(from), y = read_tr16(from + 8 * S::kPitch);
-                    o[db] = mma32(__builtin_bit_cast(X8, u32x4{x.x, x.y, y.x, y.y}), pr[t], o[db]);
-                }
+            for (int i = 0; i < 4 * NB; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                o[i % NB] = mma32(ring[i % kAhead], pr[i / NB], o[i % NB]);
+                if (i + kAhead < 4 * NB) ring[i % kAhead] = read_v(i + kAhead);
+            }
             if (__builtin_expect(taken_out[buf] == j0, 0)) {
                 // what store() has taken out, to the rows that see it
 #pragma unroll 1
