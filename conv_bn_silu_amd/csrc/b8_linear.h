@@ -20,9 +20,23 @@ struct CodesLayout {
     int64_t bytes;
 };
 CodesLayout codes_layout(void *workspace, int64_t M, int64_t K);
-hipError_t launch_quant_rows(const LinearArgs &a, const CodesLayout &l, hipStream_t st);
+// Quantises x; with `to`, also lays the rows of w out there, Kp apart.
+hipError_t launch_quant_rows(const LinearArgs &a, const CodesLayout &l, int8_t *to, hipStream_t st);
 
 #ifdef __HIPCC__
+// 16 bytes of w at byte `at`, some or all of which may lie past its `size` bytes: those
+// come as zero and are not read.
+__device__ __forceinline__ i32x4 load_end(const int8_t *w, int64_t at, int64_t size) {
+    if (at + 16 <= size) return __builtin_bit_cast(i32x4, ((const Any16 *)(w + at))->v);
+    uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+    for (int64_t i = size - 1; i >= at; --i) {
+        hi = hi << 8 | lo >> 56;
+        lo = lo << 8 | (uint8_t)w[i];
+    }
+    return i32x4{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
+}
+
 // y = act(sum * sw * sa + bias).  The sum is exact in 32-bit integers; as fp32 it
 // is rounded once (2^-24), then two products and the bias.  The weight's scale
 // goes first: the row's may be as small or large as fp32 holds, and their

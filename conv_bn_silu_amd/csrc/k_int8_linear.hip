@@ -9,30 +9,21 @@
 // so the same whatever the order.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "b8_device.h"
 #include "b8_linear.h"
 
 namespace cbs {
 namespace {
 
-// 16 bytes of w at byte `at`, some or all of which may lie past its `size` bytes: those
-// come as zero and are not read.
-__device__ __forceinline__ i32x4 load_end(const int8_t *w, int64_t at, int64_t size) {
-    if (at + 16 <= size) return __builtin_bit_cast(i32x4, ((const Any16 *)(w + at))->v);
-    uint64_t lo = 0, hi = 0;
-#pragma unroll 1
-    for (int64_t i = size - 1; i >= at; --i) {
-        hi = hi << 8 | lo >> 56;
-        lo = lo << 8 | (uint8_t)w[i];
-    }
-    return i32x4{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
-}
-
 // --- few rows --------------------------------------------------------------------
 
 constexpr int kStreamWaves = 8;
 constexpr int kStreamThreads = 64 * kStreamWaves;
-constexpr int kFusedBytes = 32768;  // codes of the fused form, in LDS
+// The fused form of linear_stream: most rows, and most codes in LDS.  4096 x 4096, fused and
+// not: 4 rows 8.5 and 9.1 us, 8 rows 11.0 and 9.2.
+constexpr int kFusedRows = 16, kFusedBytes = 16384;
 
 struct StreamParams {
     CodesLayout l;
@@ -120,11 +111,13 @@ __global__ __launch_bounds__(kStreamThreads) void linear_stream(const StreamPara
             for (int i = 0; i < 8; ++i) top = max(top, magnitude(v[i]));
         }
 #pragma unroll
-        for (int o = 1; o < 64; o *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
-        if (lane == 0) row_tops[wave] = top;
-        __syncthreads();
+        for (int o = 1; o < (kTeam < 64 ? kTeam : 64); o *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
+        if constexpr (kTeam > 64) {
+            if (lane == 0) row_tops[wave] = top;
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kTeam / 64; ++i) top = max(top, row_tops[m * (kTeam / 64) + i]);
+            for (int i = 0; i < kTeam / 64; ++i) top = max(top, row_tops[m * (kTeam / 64) + i]);
+        }
         const float s = row_scale(top), inv = row_inverse(s, top);
         if (m < p.M) {
             for (int k = t * 8; k < p.l.Kp; k += kTeam * 8) {
@@ -218,101 +211,15 @@ struct TileParams {
     int M, N, m_tiles, n_tiles;
 };
 
-typedef __attribute__((address_space(3))) void lds_void;
-
-// BM x BN outputs, a wave 32 MB x 64 of them on v_mfma_i32_32x32x32_i8; K in
-// steps of 128 through LDS, where loads write directly, one step ahead.
-//
-// An LDS row is 128 bytes of one row of an operand; its 16-byte pieces are
-// exchanged by (row / 2) % 8, so that the 16 rows that a quarter of a wave reads
-// at one k cover all banks.  The loads, which fill LDS in lane order, fetch the
-// pieces in that order from memory, through buffers that end with the operand's
-// part: rows past it come as zero.
-template <typename T, bool SILU, int BM, int BN, int MB>
-__global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64), 2) void linear_tile(const TileParams p) {
-    constexpr int kWavesN = BN / 64, kWaves = BM / (32 * MB) * kWavesN, NB = 2;
-    constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;  // of 8 rows, a wave and step
-    __shared__ __attribute__((aligned(16))) int8_t a0[BM * 128], b0[BN * 128], a1[BM * 128], b1[BN * 128];
-    const int lane = (int)threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
-    const Tile t = place((int)blockIdx.x, p.m_tiles, p.n_tiles);
-    const int m0 = t.m * BM, n0 = t.n * BN;
-
-    // staging: lane i of a load fetches the piece that belongs at i % 8 of row i / 8
-    const uint32_t block = (uint32_t)p.l.rows * 64;
-    uint32_t off_a[kLoadsA], off_b[kLoadsB];
-#pragma unroll
-    for (int i = 0; i < kLoadsA; ++i) {
-        const int r = (wave * kLoadsA + i) * 8 + lane / 8, c = (lane % 8) ^ ((r >> 1) & 7);
-        off_a[i] = c / 4 * block + (uint32_t)(r * 64 + c % 4 * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < kLoadsB; ++i) {
-        const int r = (wave * kLoadsB + i) * 8 + lane / 8, c = (lane % 8) ^ ((r >> 1) & 7);
-        off_b[i] = (uint32_t)(r * p.w_stride + c * 16);
-    }
-    const int8_t *base_a = p.l.codes + (int64_t)m0 * 64, *base_b = p.w + (int64_t)n0 * p.w_stride;
-    const uint32_t size_a = 2 * block - (uint32_t)m0 * 64, size_b = (uint32_t)(min(BN, p.N - n0) * p.w_stride);
-    auto stage = [&](int s, int8_t *a, int8_t *b) {
-        const auto ra = make_rsrc(base_a + (int64_t)s * 2 * block, size_a);
-        const auto rb = make_rsrc(base_b + s * 128, size_b - (uint32_t)s * 128);
-#pragma unroll
-        for (int i = 0; i < kLoadsA; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(a + (wave * kLoadsA + i) * 1024), 16, (int)off_a[i],
-                                                     0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < kLoadsB; ++i)  // past K: the next row or zero, against codes of zero
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(b + (wave * kLoadsB + i) * 1024), 16, (int)off_b[i],
-                                                     0, 0, 0);
-    };
-
-    const int wm = wave / kWavesN * 32 * MB, wn = wave % kWavesN * 64, r32 = lane % 32, half = lane / 32;
-    const int swap = (r32 >> 1) & 7;  // the same for every 32 rows
-    i32x16 acc[MB][NB] = {};
-    auto compute = [&](const int8_t *a, const int8_t *b) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int at = ((2 * k + half) ^ swap) * 16 + r32 * 128;
-            i32x4 af[MB], bf[NB];
-#pragma unroll
-            for (int j = 0; j < NB; ++j) bf[j] = *(const i32x4 *)(b + (wn + 32 * j) * 128 + at);
-#pragma unroll
-            for (int i = 0; i < MB; ++i) af[i] = *(const i32x4 *)(a + (wm + 32 * i) * 128 + at);
-#pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(af[i], bf[j], acc[i][j], 0, 0, 0);
-        }
-    };
-    const int steps = p.l.Kp / 128;
-    stage(0, a0, b0);
-    int s = 0;
-    for (; s + 2 < steps; s += 2) {
-        __syncthreads();  // this step's tiles are there, the other pair is free
-        stage(s + 1, a1, b1);
-        compute(a0, b0);
-        __syncthreads();
-        stage(s + 2, a0, b0);
-        compute(a1, b1);
-    }
-    __syncthreads();
-    if (s + 1 < steps) stage(s + 1, a1, b1);
-    compute(a0, b0);
-    __syncthreads();
-    if (s + 1 < steps) {
-        compute(a1, b1);
-        __syncthreads();
-    }
-
-    // A lane holds one n and, of every 32 rows, 16.  32 rows at a time go through
-    // the wave's own part of LDS (64 sums and a pad a row), so that a lane then
-    // has 8 neighbouring n and a store covers whole lines.
-    constexpr int kPitch = 68;  // sums a row
-    constexpr int kEach = kWaves / 4;
-    static_assert(kWaves % 4 == 0 && BM == BN && 32 * kPitch * 4 * kEach <= 128 * BM, "a quarter of the waves to each array");
-    int *tile = (int *)(wave / kEach == 0 ? a0 : wave / kEach == 1 ? b0 : wave / kEach == 2 ? a1 : b1) +
-                wave % kEach * (32 * kPitch);
-    const int n = n0 + wn + lane % 8 * 8;
+// Stores a wave's sums, 32 MB x 64 of them from (m0, n0).  A lane holds one n and, of every
+// 32 rows, 16.  32 rows at a time go through the wave's own part of LDS (64 sums
+// and a pad a row), so that a lane then has 8 neighbouring n and a store covers
+// whole lines.
+constexpr int kTilePitch = 68, kTileBytes = 32 * kTilePitch * 4;
+template <typename T, bool SILU, int MB>
+__device__ __forceinline__ void store_sums(const TileParams &p, const i32x16 (&acc)[MB][2], int *tile, int m0, int n0) {
+    const int lane = (int)threadIdx.x % 64, r32 = lane % 32, half = lane / 32;
+    const int n = n0 + lane % 8 * 8;
     float sw[8], bias[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -322,15 +229,15 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64), 2) void linear_t
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                tile[(8 * (r / 4) + 4 * half + r % 4) * kPitch + 32 * j + r32] = acc[i][j][r];
+                tile[(8 * (r / 4) + 4 * half + r % 4) * kTilePitch + 32 * j + r32] = acc[i][j][r];
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int row = 8 * q + lane / 8, m = m0 + wm + 32 * i + row;
-            const i32x4 *from = (const i32x4 *)(tile + row * kPitch + lane % 8 * 8);
+            const int row = 8 * q + lane / 8, m = m0 + 32 * i + row;
+            const i32x4 *from = (const i32x4 *)(tile + row * kTilePitch + lane % 8 * 8);
             const i32x4 lo = from[0], hi = from[1];
             if (m >= p.M) continue;
             const float sa = p.l.scales[m];
@@ -351,29 +258,222 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64), 2) void linear_t
     }
 }
 
-// Rows of w at any byte to rows of Kp, each at a multiple of 16, for the tile kernel's
-// loads.
-__global__ __launch_bounds__(256) void align_rows(const int8_t *__restrict__ w, int8_t *__restrict__ to, int N, int K,
-                                                  int Kp) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int each = Kp / 16;
-    const int64_t n = i / each;
-    if (n >= N) return;
-    const int k = (int)(i - n * each) * 16;
-    *(i32x4 *)(to + n * Kp + k) = load_end(w, n * K + k, (int64_t)N * K);
+typedef __attribute__((address_space(3))) void lds_void;
+
+// A step's products of a wave, from its rows of the two operands in LDS.  The fragments
+// of AHEAD of the step's four parts are on their way at a time, and `issue` (a quarter of a
+// later step's loads) goes between the parts; the order is held.  Left alone the compiler
+// reads a part when it is wanted, and the matrix pipe waits for each; and loads issued all
+// at once hold the wave up for as long as the CU takes to serve them (64 bytes a
+// clock: half of a step).
+template <int MB, int AHEAD, typename F>
+__device__ __forceinline__ void multiply(i32x16 (&acc)[MB][2], const int8_t *a, const int8_t *b, int half, int swap,
+                                         F &&issue) {
+    i32x4 af[AHEAD][MB], bf[AHEAD][2];
+    auto read = [&](int k) {
+        const int at = ((2 * k + half) ^ swap) * 16;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) bf[k % AHEAD][j] = *(const i32x4 *)(b + 32 * j * 128 + at);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) af[k % AHEAD][i] = *(const i32x4 *)(a + 32 * i * 128 + at);
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) read(k);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        __builtin_amdgcn_sched_barrier(0);
+        issue(k);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(af[k % AHEAD][i], bf[k % AHEAD][j], acc[i][j], 0, 0, 0);
+        if (k + AHEAD < 4) {
+            __builtin_amdgcn_sched_barrier(0);
+            read(k + AHEAD);
+        }
+    }
+}
+
+// Where a wave's loads of an operand's step come from and go: load i fills 8 rows of 128
+// bytes; lane j of it fetches the piece that belongs at j % 8 of row j / 8.
+//
+// An LDS row's 16-byte pieces are exchanged by (row / 2) % 8, so that the 16 rows that a
+// quarter of a wave reads at one k cover all banks.  The loads, which fill LDS in lane
+// order, fetch the pieces in that order from memory, through buffers that end with the
+// operand's part: rows past it come as zero, and a buffer of no bytes is a step past
+// the last.
+constexpr int kLoads = 4;  // of each operand, a wave and step
+struct Loads {
+    const int8_t *base_a, *base_b;
+    uint32_t off_a[kLoads], off_b[kLoads], size_a, size_b;
+    int64_t step_a;
+    int wave, steps;
+    __device__ __forceinline__ Loads(const TileParams &p, int m0, int n0, int bn, int w, int lane) {
+        const uint32_t block = (uint32_t)p.l.rows * 64;
+        wave = w, steps = p.l.Kp / 128;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = (wave * kLoads + i) * 8 + lane / 8, c = (lane % 8) ^ ((r >> 1) & 7);
+            off_a[i] = c / 4 * block + (uint32_t)(r * 64 + c % 4 * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = (wave * kLoads + i) * 8 + lane / 8, c = (lane % 8) ^ ((r >> 1) & 7);
+            off_b[i] = (uint32_t)(r * p.w_stride + c * 16);
+        }
+        base_a = p.l.codes + (int64_t)m0 * 64, base_b = p.w + (int64_t)n0 * p.w_stride;
+        step_a = 2 * (int64_t)block;
+        size_a = 2 * block - (uint32_t)m0 * 64, size_b = (uint32_t)(min(bn, p.N - n0) * p.w_stride);
+    }
+    // A step's part of the operands, and its size.
+    __device__ __forceinline__ const int8_t *a_at(int s) const { return base_a + s * step_a; }
+    __device__ __forceinline__ const int8_t *b_at(int s) const { return base_b + s * 128; }
+    __device__ __forceinline__ uint32_t a_bytes(int s) const { return __builtin_amdgcn_readfirstlane(s < steps ? size_a : 0); }
+    __device__ __forceinline__ uint32_t b_bytes(int s) const {
+        return __builtin_amdgcn_readfirstlane(s < steps ? size_b - (uint32_t)s * 128 : 0);
+    }
+};
+
+// BM x BN outputs, a wave 32 MB x 64 of them on v_mfma_i32_32x32x32_i8; K in
+// steps of 128 through LDS, where loads write directly, one step ahead.
+template <typename T, bool SILU, int BM, int BN, int MB>
+__global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64), 2) void linear_tile(const TileParams p) {
+    constexpr int kWavesN = BN / 64, kWaves = BM / (32 * MB) * kWavesN;
+    static_assert(BM == BN && BM / 8 / kWaves == kLoads, "");
+    __shared__ __attribute__((aligned(16))) int8_t a0[BM * 128], b0[BN * 128], a1[BM * 128], b1[BN * 128];
+    const int lane = (int)threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+    const Tile t = place((int)blockIdx.x, p.m_tiles, p.n_tiles);
+    const int m0 = t.m * BM, n0 = t.n * BN;
+    const Loads loads(p, m0, n0, BN, wave, lane);
+    const int wm = wave / kWavesN * 32 * MB, wn = wave % kWavesN * 64, r32 = lane % 32, half = lane / 32;
+    const int swap = (r32 >> 1) & 7;  // the same for every 32 rows
+    const int at_a = (wm + r32) * 128, at_b = (wn + r32) * 128;
+    i32x16 acc[MB][2] = {};
+    // Load i of either operand of step s.  Past K the next row of w or zero comes, against codes of zero.
+    auto issue = [&](int s, int i, int8_t *a, int8_t *b) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(loads.a_at(s), loads.a_bytes(s)), (lds_void *)(a + (wave * kLoads + i) * 1024), 16,
+                                                 (int)loads.off_a[i], 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(loads.b_at(s), loads.b_bytes(s)), (lds_void *)(b + (wave * kLoads + i) * 1024), 16,
+                                                 (int)loads.off_b[i], 0, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) issue(0, i, a0, b0);
+    for (int s = 0; s < loads.steps; s += 2) {
+        __syncthreads();  // this step's tiles are there, the other pair is free
+        multiply<MB, 2>(acc, a0 + at_a, b0 + at_b, half, swap, [&](int k) { issue(s + 1, k, a1, b1); });
+        __syncthreads();
+        if (s + 1 < loads.steps)
+            multiply<MB, 2>(acc, a1 + at_a, b1 + at_b, half, swap, [&](int k) { issue(s + 2, k, a0, b0); });
+    }
+    __syncthreads();
+    constexpr int kEach = kWaves / 4;
+    static_assert(kWaves % 4 == 0 && kTileBytes * kEach <= 128 * BM, "a quarter of the waves to each array");
+    int8_t *const mine = wave / kEach == 0 ? a0 : wave / kEach == 1 ? b0 : wave / kEach == 2 ? a1 : b1;
+    store_sums<T, SILU, MB>(p, acc, (int *)(mine + wave % kEach * kTileBytes), m0 + wm, n0 + wn);
+}
+
+// The same for fewer tiles than keep every CU's matrix pipes fed: then a step is done long
+// before the next one's loads arrive, so that here the loads run four steps ahead, in
+// registers (which a wave has to spare), and pass into one of two LDS buffers a
+// step ahead.
+template <typename T, bool SILU, int BM, int BN, int MB>
+__global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64)) void linear_ring(const TileParams p) {
+    constexpr int kWavesN = BN / 64, kWaves = BM / (32 * MB) * kWavesN;
+    constexpr int kSets = 4;
+    static_assert(BM == BN && BM / 8 / kWaves == kLoads, "");
+    constexpr int kB = BM * 128;  // where a buffer's part of w begins
+    __shared__ __attribute__((aligned(16))) int8_t lds[2][2 * kB];
+    const int lane = (int)threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+    const Tile t = place((int)blockIdx.x, p.m_tiles, p.n_tiles);
+    const int m0 = t.m * BM, n0 = t.n * BN;
+    const Loads loads(p, m0, n0, BN, wave, lane);
+    const int wm = wave / kWavesN * 32 * MB, wn = wave % kWavesN * 64, r32 = lane % 32, half = lane / 32;
+    const int swap = (r32 >> 1) & 7;
+    i32x16 acc[MB][2] = {};
+    u32x4 ra[kSets][kLoads], rb[kSets][kLoads];
+    const int to = wave * kLoads * 1024 + lane * 16;
+    auto fetch = [&](int s, int set, int i) {
+        ra[set][i] = buf_load16(make_rsrc(loads.a_at(s), loads.a_bytes(s)), loads.off_a[i]);
+        rb[set][i] = buf_load16(make_rsrc(loads.b_at(s), loads.b_bytes(s)), loads.off_b[i]);
+    };
+    auto pass = [&](int set, int i, int8_t *buf) {
+        *(u32x4 *)(buf + to + i * 1024) = ra[set][i];
+        *(u32x4 *)(buf + kB + to + i * 1024) = rb[set][i];
+    };
+    auto turn = [&](int s, auto turn_of_4) {
+        constexpr int kNow = decltype(turn_of_4)::value, kNext = (kNow + 1) % kSets;
+        const int8_t *const buf = lds[kNow % 2];
+        // what this wave has written is there (lgkmcnt(0); loads go on), and so is what the others have
+        __builtin_amdgcn_s_waitcnt(15 | 3 << 14 | 7 << 4);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        multiply<MB, 2>(acc, buf + (wm + r32) * 128, buf + kB + (wn + r32) * 128, half, swap, [&](int k) {
+            pass(kNext, k, lds[1 - kNow % 2]);
+            fetch(s + 1 + kSets, kNext, k);
+        });
+    };
+    // in this order: the waits in the loop count on it
+#pragma unroll
+    for (int set = 0; set < kSets; ++set)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            fetch(set, set, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        pass(0, i, lds[0]);
+        fetch(kSets, 0, i);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    using std::integral_constant;
+    int s = 0;
+    for (; s + 4 <= loads.steps; s += 4) {  // without a way out in between, where the waits would have to be for the worst
+        turn(s, integral_constant<int, 0>{});
+        turn(s + 1, integral_constant<int, 1>{});
+        turn(s + 2, integral_constant<int, 2>{});
+        turn(s + 3, integral_constant<int, 3>{});
+    }
+    if (s < loads.steps) turn(s, integral_constant<int, 0>{});
+    if (s + 1 < loads.steps) turn(s + 1, integral_constant<int, 1>{});
+    if (s + 2 < loads.steps) turn(s + 2, integral_constant<int, 2>{});
+    __syncthreads();
+    static_assert(kTileBytes * kWaves <= 4 * kB, "");
+    store_sums<T, SILU, MB>(p, acc, (int *)(lds[0] + wave * kTileBytes), m0 + wm, n0 + wn);
 }
 
 // --- choice ----------------------------------------------------------------------
 
-enum Kind { kStream, kTile128, kTile256 };
-// By the number of tiles that a kernel makes of the output, against the 256 CUs.
-Kind kind_of(int64_t M, int64_t N) {
-    const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256), t128 = ((M + 127) / 128) * ((N + 127) / 128);
-    if (M <= 64) return kStream;
-    if (t256 >= 192) return kTile256;
-    return t128 >= 128 ? kTile128 : kStream;
+// By the number of tiles that a kernel makes of the output, against the 256 CUs.  Where
+// the choice changes, measured at K 2048 and 8192, in us:
+//   M x N         linear_stream   ring 64       ring 128      tile 256
+//   64 x 4096     10.0, 19.9      11.8, 24.2
+//   96 x 4096     12.4, 28.3      12.2, 24.6
+//   512 x 4096    29.4, 73.6      16.9, 35.1    19.5, 40.8
+//   768 x 4096    40.4, 106       20.7, 47.8    20.5, 43.6
+//   32 x 8192     10.9, 22.1      12.0, 23.2
+//   32 x 16384    13.5, 37.9      12.9, 28.3
+//   2048 x 8192   (K 4096)        117           86.3          70.4
+enum Kind { kStream, kRing64, kRing128, kTile256 };
+// Rows of the fused form for M rows of x, 0 where it does not serve them.
+int fused_rows(int64_t M, int64_t K) {
+    int rows = 1;
+    while (rows < M) rows *= 2;
+    return rows <= kFusedRows && rows * ((K + 127) / 128 * 128) <= kFusedBytes ? rows : 0;
 }
-bool needs_copy(int64_t M, int64_t N, int64_t K) { return K % 16 != 0 && kind_of(M, N) != kStream; }
+int64_t tiles(int64_t M, int64_t N, int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); }
+Kind kind_of(int64_t M, int64_t N, int64_t K) {
+    if (fused_rows(M, K)) return kStream;
+    // rows of w that start at odd bytes are read by linear_stream as they are, and have to be copied for the others
+    if (K % 16 != 0 && M <= 128) return kStream;
+    if (tiles(M, N, 256) >= 192) return kTile256;
+    if (tiles(M, N, 128) >= 160) return kRing128;
+    return tiles(M, N, 64) >= (M <= 32 ? 256 : 96) ? kRing64 : kStream;
+}
+bool needs_copy(int64_t M, int64_t N, int64_t K) { return K % 16 != 0 && kind_of(M, N, K) != kStream; }
 
 template <typename T, int MT, int NT, int ROWS> hipError_t launch_stream4(const StreamParams &p, hipStream_t st) {
     const dim3 grid((p.N + 16 * NT - 1) / (16 * NT), (p.M + 16 * MT - 1) / (16 * MT));
@@ -388,10 +488,14 @@ template <typename T, int MT, int ROWS> hipError_t launch_stream3(const StreamPa
 }
 template <typename T> hipError_t launch_stream(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
     const StreamParams p{l, a.w, a.w_scale, a.bias, a.x, a.x_stride, a.y, a.M, a.N, a.K, a.dtype, a.act};
-    if (a.M <= 1 && (int64_t)l.Kp <= kFusedBytes) return launch_stream3<T, 1, 1>(p, st);
-    if (a.M <= 2 && (int64_t)l.Kp * 2 <= kFusedBytes) return launch_stream3<T, 1, 2>(p, st);
-    if (a.M <= 4 && (int64_t)l.Kp * 4 <= kFusedBytes) return launch_stream3<T, 1, 4>(p, st);
-    const hipError_t e = launch_quant_rows(a, l, st);
+    switch (fused_rows(a.M, a.K)) {
+        case 1: return launch_stream3<T, 1, 1>(p, st);
+        case 2: return launch_stream3<T, 1, 2>(p, st);
+        case 4: return launch_stream3<T, 1, 4>(p, st);
+        case 8: return launch_stream3<T, 1, 8>(p, st);
+        case 16: return launch_stream3<T, 1, 16>(p, st);
+    }
+    const hipError_t e = launch_quant_rows(a, l, nullptr, st);
     if (e != hipSuccess) return e;
     // from here on x is not read: one type of the kernel serves all
     if (a.M <= 16) return launch_stream3<float, 1, 0>(p, st);
@@ -401,24 +505,21 @@ template <typename T> hipError_t launch_stream(const LinearArgs &a, const CodesL
 }
 
 template <typename T, bool SILU> hipError_t launch2(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
-    const Kind kind = kind_of(a.M, a.N);
+    const Kind kind = kind_of(a.M, a.N, a.K);
     const bool copy = needs_copy(a.M, a.N, a.K);
     // where only w's start is off 16 bytes there is no room for a copy
     if (kind == kStream || (!copy && (uintptr_t)a.w % 16 != 0)) return launch_stream<T>(a, l, st);
-    hipError_t e = launch_quant_rows(a, l, st);
-    if (e != hipSuccess) return e;
     TileParams p{l, a.w, a.K, a.w_scale, a.bias, a.y, a.M, a.N, 0, 0};
-    if (copy) {
-        int8_t *to = l.codes + (int64_t)l.rows * l.Kp;
-        align_rows<<<(unsigned)(((int64_t)a.N * (l.Kp / 16) + 255) / 256), 256, 0, st>>>(a.w, to, a.N, a.K, l.Kp);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        p.w = to, p.w_stride = l.Kp;
-    }
-    const int b = kind == kTile256 ? 256 : 128;
+    int8_t *const to = copy ? l.codes + (int64_t)l.rows * l.Kp : nullptr;
+    const hipError_t e = launch_quant_rows(a, l, to, st);
+    if (e != hipSuccess) return e;
+    if (copy) p.w = to, p.w_stride = l.Kp;
+    const int b = kind == kTile256 ? 256 : kind == kRing128 ? 128 : 64;
     p.m_tiles = (a.M + b - 1) / b, p.n_tiles = (a.N + b - 1) / b;
     const unsigned grid = (unsigned)(p.m_tiles * p.n_tiles);
     if (kind == kTile256) linear_tile<T, SILU, 256, 256, 4><<<grid, 512, 0, st>>>(p);
-    else linear_tile<T, SILU, 128, 128, 2><<<grid, 256, 0, st>>>(p);
+    else if (kind == kRing128) linear_ring<T, SILU, 128, 128, 2><<<grid, 256, 0, st>>>(p);
+    else linear_ring<T, SILU, 64, 64, 1><<<grid, 128, 0, st>>>(p);
     return hipGetLastError();
 }
 template <typename T> hipError_t launch1(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {

@@ -81,6 +81,22 @@ def test_linear_strides_and_alignment(ops, shape):
         O.check(ops.int8_linear(xt, w.cuda(), ws.cuda(), b.cuda()), ref, tol, f"{shape} transposed")
 
 
+@pytest.mark.parametrize("shape", [
+    # M, N, K: each kernel's own sizes, off its tiles: rows quantised inside the product (up to 16), tiles of 64, of
+    # 128 and of 256, K from one step to several rounds of the buffers, rows of w at odd bytes
+    (6, 300, 2000), (9, 70, 900), (16, 500, 1024), (16, 500, 1040), (7, 40, 131072), (20, 16390, 48), (64, 16400, 640),
+    (97, 4097, 1152), (130, 3100, 130), (140, 5000, 1023), (1300, 2001, 128), (1281, 2050, 784), (1400, 1999, 515),
+    (3500, 3460, 16), (4097, 3011, 144), (3400, 3600, 129),
+], ids=lambda s: "x".join(map(str, s)))
+def test_linear_kernels(ops, shape):
+    M, N, K = shape
+    for dtype, bias, act in ((BF16, False, None), (F32, True, "silu")):
+        say("[linear kernels]", shape, dtype)
+        x, w, ws, b = linear_inputs(M, N, K, dtype, M + N + K)
+        ref, tol = O.linear(x, w, ws, b if bias else None, act == "silu")
+        O.check(ops.int8_linear(x.cuda(), w.cuda(), ws.cuda(), b.cuda() if bias else None, act), ref, tol, f"{shape}")
+
+
 def test_linear_leading_axes_and_empty(ops):
     x, w, ws, b = linear_inputs(24, 48, 64, BF16, 5)
     ref, tol = O.linear(x, w, ws, b, True)
