@@ -9,7 +9,7 @@
 namespace cbs {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
 // One row: its chunks' parts, brought to one maximum and added.  A wave to a row: its
 // lanes are the chunks where maxima and sums are concerned, and the dims for the outputs,
@@ -61,13 +61,14 @@ __device__ __forceinline__ void join(const AttentionPlan &p, const AttentionPart
     else join_dims<T, 4>(p, part, line, n, out);
 }
 
-// A workgroup to a sequence and key/value head.
-template <typename T> __global__ __launch_bounds__(kThreads) void join_few(const AttentionPlan p) {
-    const int kvh = (int)blockIdx.x % p.a.cache.heads, wave = (int)threadIdx.x / 64;
-    const Sequence s = sequence(p, (int)blockIdx.x / p.a.cache.heads);
+// A wave to a row of a sequence and key/value head; beside attend_many, there is at most a tile of them.
+template <typename T> __device__ __forceinline__ void join_few(const AttentionPlan &p, int at) {
+    const int per = (p.few.tile + kWaves - 1) / kWaves, pair = at / per, wave = (int)threadIdx.x / 64;
+    const int kvh = pair % p.a.cache.heads;
+    const Sequence s = sequence(p, pair / p.a.cache.heads);
     const int rows = s.n * (int)p.group.d;
     if (is_many(p, rows)) return;
-    for (int r = wave; r < rows; r += kThreads / 64) {
+    for (int r = at % per * kWaves + wave; r < rows; r += per * kWaves) {
         const int r0 = r / p.few.tile * p.few.tile;
         const int n = chunks_of(p.few, keys_of(p, s, r0, min(rows, r0 + p.few.tile)));
         if (n > 1) join<T>(p, p.few, few_line(p, s, kvh, r), n, out_line(p, s, kvh, r));
@@ -75,9 +76,9 @@ template <typename T> __global__ __launch_bounds__(kThreads) void join_few(const
 }
 
 // A wave to a row of the output.
-template <typename T> __global__ __launch_bounds__(kThreads) void join_many(const AttentionPlan p) {
+template <typename T> __device__ __forceinline__ void join_many(const AttentionPlan &p, int at) {
     const int lane = (int)threadIdx.x % 64;
-    const int64_t line = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+    const int64_t line = (int64_t)at * kWaves + threadIdx.x / 64;
     if (line >= (int64_t)p.a.tokens * p.a.heads) return;
     const int token = (int)(line / p.a.heads), head = (int)(line - (int64_t)token * p.a.heads);
     const int kvh = (int)p.group.div((uint32_t)head);
@@ -96,6 +97,12 @@ template <typename T> __global__ __launch_bounds__(kThreads) void join_many(cons
     }
 }
 
+// The first `few` workgroups have attend_few's rows, the others attend_many's.
+template <typename T> __global__ __launch_bounds__(kThreads) void join_parts(const AttentionPlan p, int few) {
+    if ((int)blockIdx.x < few) join_few<T>(p, (int)blockIdx.x);
+    else join_many<T>(p, (int)blockIdx.x - few);
+}
+
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // Lays a kernel's parts out in the workspace, `at` floats of which are taken.
 void place_parts(AttentionPart &part, float *ws, int64_t &at, int64_t lines, int64_t dim) {
@@ -110,8 +117,9 @@ void place_parts(AttentionPart &part, float *ws, int64_t &at, int64_t lines, int
 int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
                   int64_t page_size, int64_t table_width, int64_t num_cu, float *ws) {
     const int64_t group = heads / kv_heads, limit = table_width * page_size, pairs = batch * kv_heads;
-    // 32 rows only where single tokens do not fill 16: the registers they take cost waves
-    p.few.tile = dim <= 128 && (tokens > batch || group > 16) ? 32 : 16;
+    // 32 rows only where the average sequence has more than 16: the registers they take cost
+    // waves (8 sequences of 2 tokens, groups of 4, over 3000 keys: 41 us, with 16 rows 25)
+    p.few.tile = dim <= 128 && tokens * group > 16 * batch ? 32 : 16;
     p.many.tile = many_tile(dim);
     // with no more tokens than sequences they are single tokens, as a rule
     p.few_only = tokens <= batch || tokens * group <= p.few.tile;
@@ -137,11 +145,10 @@ int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads
 }
 
 template <typename T> hipError_t launch_joins(const AttentionPlan &p, hipStream_t st) {
-    if (p.few.chunks > 1) join_few<T><<<(unsigned)(p.a.batch * p.a.cache.heads), kThreads, 0, st>>>(p);
-    if (!p.few_only && p.many.chunks > 1) {
-        const int64_t lines = (int64_t)p.a.tokens * p.a.heads;
-        join_many<T><<<(unsigned)((lines + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, st>>>(p);
-    }
+    const int64_t lines = !p.few_only && p.many.chunks > 1 ? (int64_t)p.a.tokens * p.a.heads : 0;
+    const int64_t many = (lines + kWaves - 1) / kWaves;
+    const int64_t few = p.few.chunks > 1 ? (int64_t)p.a.batch * p.a.cache.heads * ((p.few.tile + kWaves - 1) / kWaves) : 0;
+    if (few + many > 0) join_parts<T><<<(unsigned)(few + many), kThreads, 0, st>>>(p, (int)few);
     return hipGetLastError();
 }
 
