@@ -132,11 +132,14 @@ int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads
     if (limit <= 1024) p.few.chunk = 1024;
     p.few.chunks = (int)std::max<int64_t>(1, (limit + p.few.chunk - 1) / p.few.chunk);
 
-    // attend_many: chunks only where there are too few tiles for the CUs
-    const int64_t groups = std::max<int64_t>(1, p.slots * kv_heads), want = groups >= num_cu ? 1 : (2 * num_cu + groups - 1) / groups;
-    p.many.chunk = (int)std::max<int64_t>(512, round_up((limit + want - 1) / want, 64));
-    p.many.chunks = (int)std::max<int64_t>(1, (limit + p.many.chunk - 1) / p.many.chunk);
-    if (want == 1) p.many.chunk = 1 << 30, p.many.chunks = 1;
+    // attend_many: chunks only where there are too few tiles for the CUs, and no more
+    // workgroups than CUs, each of which holds one (512 tokens after 4000, 8 heads over 2: 162
+    // workgroups 43 us, 252 40, 324 54).  Of the tiles that may be partial, half count.
+    const int64_t partial = std::min(batch, tokens * group / (p.few.tile + 1));
+    const int64_t groups2 = std::max<int64_t>(1, (2 * tokens * group / p.many.tile + partial) * kv_heads);
+    const int64_t want = limit <= 512 ? 1 : std::max<int64_t>(1, 2 * num_cu / groups2);
+    p.many.chunk = want == 1 ? 1 << 30 : (int)std::max<int64_t>(256, round_up((limit + want - 1) / want, 64));
+    p.many.chunks = want == 1 ? 1 : (int)std::max<int64_t>(1, (limit + p.many.chunk - 1) / p.many.chunk);
 
     int64_t at = 0;
     place_parts(p.few, ws, at, p.few_only ? tokens * heads : pairs * p.few.tile, dim);

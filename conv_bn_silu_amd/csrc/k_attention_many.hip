@@ -409,25 +409,40 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     // the lane has one row, of every 32 dims 16
     const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     const float sum = __uint_as_float(both[0]) + __uint_as_float(both[1]);
-    const int mine = r0 + 32 * wave + col;
-    if (n_chunks > 1) {
-        if (mine >= r1) return;
-        const int64_t line = out_line(p, seq, kvh, mine) * p.many.chunks + c;
-#pragma unroll
-        for (int db = 0; db < NB; ++db)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int d = 32 * db + 8 * g + 4 * half;
-                f32x4 v = {o[db][4 * g], o[db][4 * g + 1], o[db][4 * g + 2], o[db][4 * g + 3]};
-                if constexpr (S::kI8) v *= o_ref;
-                if (d < dim) *(f32x4 *)(p.many.o + line * dim + d) = v;
-            }
-        if (half == 0) p.many.ml[2 * line] = m == -INFINITY ? -INFINITY : m * qf, p.many.ml[2 * line + 1] = sum;
-        return;
-    }
+    // Through LDS, so that a row's dims are stored side by side; parts, in fp32, half of them at a time.
     __syncthreads();
     unsigned char *const stage = lds + wave * 32 * S::kOutPitch;
     const float ref = S::kI8 ? o_ref : 1.f;
+    constexpr int kOutPieces = S::kPitch / 16;
+    if (n_chunks > 1) {
+        constexpr int kHalf = S::kPitchDims / 2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int db = 0; db < NB; ++db)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (32 * db / kHalf != h) continue;
+                    const f32x4 v = {o[db][4 * g], o[db][4 * g + 1], o[db][4 * g + 2], o[db][4 * g + 3]};
+                    *(f32x4 *)(stage + col * S::kOutPitch + 4 * (32 * db - h * kHalf + 8 * g + 4 * half)) = v * ref;
+                }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+            for (int i = lane; i < 32 * kOutPieces; i += 64) {
+                const int row = i / kOutPieces, d = h * kHalf + i % kOutPieces * 4, at = r0 + 32 * wave + row;
+                if (at < r1 && d < dim)
+                    *(f32x4 *)(p.many.o + (out_line(p, seq, kvh, at) * p.many.chunks + c) * dim + d) =
+                        *(const f32x4 *)(stage + row * S::kOutPitch + i % kOutPieces * 16);
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+        const int mine = r0 + 32 * wave + col;
+        if (half == 0 && mine < r1) {
+            const int64_t line = out_line(p, seq, kvh, mine) * p.many.chunks + c;
+            p.many.ml[2 * line] = m == -INFINITY ? -INFINITY : m * qf, p.many.ml[2 * line + 1] = sum;
+        }
+        return;
+    }
 #pragma unroll
     for (int db = 0; db < NB; ++db)
 #pragma unroll
@@ -439,7 +454,6 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
             *(x4 *)(stage + col * S::kOutPitch + 2 * (32 * db + 8 * g + 4 * half)) = v;
         }
     __builtin_amdgcn_wave_barrier();
-    constexpr int kOutPieces = S::kPitch / 16;
 #pragma unroll 1
     for (int i = lane; i < 32 * kOutPieces; i += 64) {
         const int row = i / kOutPieces, d = i % kOutPieces * 8, at = r0 + 32 * wave + row;
