@@ -85,6 +85,8 @@ int check_attention_sizes(int64_t batch, int64_t tokens, int64_t heads, int64_t 
     // numbers in the kernels, with room for a tile more
     const int64_t group = heads / kv_heads, lim = 1 << 30;
     if (tokens > lim / group || table_width > lim / group / page_size) return CBS_ERR_UNSUPPORTED;
+    // and the launches' workgroups fit a grid
+    if (tokens > (1 << 29) / heads || batch > (1 << 20) / kv_heads) return CBS_ERR_UNSUPPORTED;
     return CBS_OK;
 }
 

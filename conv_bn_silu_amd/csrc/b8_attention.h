@@ -166,6 +166,9 @@ template <typename X> struct Parts {
     }
 };
 
+// A key's scale: under an infinite one its elements are infinities of both signs, or NaN
+// where the code is 0, and so its score is NaN, not the infinity that scaling the sum gives.
+__device__ __forceinline__ float finite_or_nan(float s) { return __builtin_isfinite(s) ? s : NAN; }
 // A power of two above the scale with these bits (a finite one), at most 2^127.
 __device__ __forceinline__ float power_above(uint32_t bits) {
     return __uint_as_float(min((bits & 0x7F800000u) + 0x00800000u, 0x7F000000u));

@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                     fade_v = vref / now;
                     vref = now;
                 }
-                kscale[lane % KT] = ks;
+                kscale[lane % KT] = finite_or_nan(ks);
                 vscale[lane % KT] = vs * (1.f / vref);
             }
             // LDS addresses are made anew for each tile: kept, they cost a register for each access

@@ -251,7 +251,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                     for (int x = 1; x < 64; x *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, x, 64));
                     vref = power_above(top);
                 }
-                kscale[buf][lane] = ks;
+                kscale[buf][lane] = finite_or_nan(ks);
                 vscale[buf][lane] = vs * (1.f / vref);
                 if (lane == 0) vrefs[buf] = vref;
             }

@@ -98,7 +98,9 @@ int cbs_cache_read(conv_bn_silu_t handle, const cbs_paged_cache *cache, const in
  * Keys past lens[b], past the table's width or on a page outside [0, pages) are
  * not seen, and what the cache holds there is never used.  Rows of out that
  * belong to no sequence are left as they are.  starts and lens are read on the
- * device, so the call never waits for them.
+ * device, so the call never waits for them.  tokens * heads up to 2^29, batch *
+ * cache heads up to 2^20 (batch up to 65536), table_width * page_size * heads /
+ * cache heads up to 2^30, else CBS_ERR_UNSUPPORTED.
  *   workspace: at least cbs_paged_attention_workspace(...) bytes, 16-byte
  *      aligned; content before and after does not matter. */
 int cbs_paged_attention(conv_bn_silu_t handle, const void *q, int64_t q_token_stride, int64_t q_head_stride,

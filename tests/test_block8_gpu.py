@@ -86,7 +86,7 @@ def test_linear_strides_and_alignment(ops, shape):
     # 128 and of 256, K from one step to several rounds of the buffers, rows of w at odd bytes
     (6, 300, 2000), (9, 70, 900), (16, 500, 1024), (16, 500, 1040), (7, 40, 131072), (20, 16390, 48), (64, 16400, 640),
     (97, 4097, 1152), (130, 3100, 130), (140, 5000, 1023), (1300, 2001, 128), (1281, 2050, 784), (1400, 1999, 515),
-    (3500, 3460, 16), (4097, 3011, 144), (3400, 3600, 129),
+    (3500, 3460, 16), (4097, 3011, 144), (3400, 3600, 129), (60, 16390, 131),
 ], ids=lambda s: "x".join(map(str, s)))
 def test_linear_kernels(ops, shape):
     M, N, K = shape
@@ -513,3 +513,113 @@ def test_attention_is_deterministic(ops):
     first = run_case(ops, c)
     for _ in range(3):
         assert torch.equal(run_case(ops, c), first)
+
+
+def test_attention_wide_table(ops):
+    """A table with room for far more tokens than any sequence has."""
+    for new, lens in (([1, 1, 1], [700, 30, 2100]), ([1, 40, 300], [2000, 40, 900])):
+        c = attention_case(new, lens, 8, 2, 64, 16, BF16, True, seed=31)
+        want = run_case(ops, c)
+        ref, tol, mine = O.attention(c["q"], *c["kv64"], c["table"], c["starts"], c["lens"], 0, c["scale"], O.half_step(F16))
+        wide = torch.full((3, 20000), -1, dtype=torch.int32)
+        wide[:, :c["table"].shape[1]] = c["table"]
+        c["table"] = wide
+        say("[attention wide table]", new)
+        O.check(run_case(ops, c), ref, tol, f"wide table {new}")
+        O.check(want, ref, tol, f"narrow table {new}")
+
+
+@pytest.mark.parametrize("dim", [16, 48, 80, 96, 112, 144, 192, 256])
+def test_attention_dims(ops, dim):
+    """Every padding of dim, single tokens and chunks, NaN in what is never read."""
+    for types in TYPES:
+        for new in ([1, 1], [70, 5]):
+            c = attention_case(new, [150, 90], 6, 2, dim, 20, *types, window=70, seed=dim)
+            check_case(ops, c, f"dim {dim} {new} {types}")
+
+
+@pytest.mark.parametrize("new,lens", [([1, 1], [900, 40]), ([5, 9], [600, 9]), ([80, 300], [500, 300])],
+                         ids=["decode", "few", "chunk"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attention_bad_scales(ops, new, lens, bad):
+    """An infinite or NaN scale of a key or value reaches the queries that see it and no others."""
+    for which in (2, 3):
+        c = attention_case(new, lens, 8, 2, 64, 16, BF16, True, seed=41)
+        ref, tol, _ = O.attention(c["q"], *c["kv64"], c["table"], c["starts"], c["lens"], 0, c["scale"], O.half_step(F16))
+        at = lens[1] - 2  # of the second sequence
+        c["tensors"][which][int(c["table"][1, at // 16]), :, at % 16] = bad
+        out = run_case(ops, c).cpu()
+        token = torch.arange(out.shape[0])
+        pos = lens[1] - new[1] + token - new[0]
+        hit = (token >= new[0]) & (pos >= at)
+        say("[attention bad scales]", new, which, bad)
+        O.check(out[~hit], ref[~hit], tol[~hit], f"rows that do not see it {new} {which}")
+        assert not bool(out[hit].isfinite().any())
+
+
+def test_refusals(ops):
+    """What the binding and the C ABI do not serve is refused before any kernel."""
+    from conv_bn_silu_amd.binding import CbsError
+    dev = dict(device="cuda")
+    x, w, s = torch.zeros(4, 64, dtype=BF16, **dev), torch.zeros(8, 64, dtype=I8, **dev), torch.zeros(8, **dev)
+    for bad in (dict(x=x.double()), dict(w=w.float()), dict(w_scale=s.half()), dict(bias=s.half()), dict(x=None),
+                dict(out=torch.zeros(4, 8, dtype=F16, **dev))):
+        with pytest.raises(TypeError):
+            ops.int8_linear(**{**dict(x=x, w=w, w_scale=s), **bad})
+    for bad in (dict(x=x[:, :63]), dict(w=w[:, ::2]), dict(w=w.t().contiguous().t()), dict(w_scale=s[:7]),
+                dict(bias=s.cpu()), dict(activation="gelu"), dict(out=torch.zeros(3, 8, dtype=BF16, **dev)),
+                dict(x=torch.zeros(4, 64, dtype=BF16, requires_grad=True, **dev))):
+        with pytest.raises(ValueError):
+            ops.int8_linear(**{**dict(x=x, w=w, w_scale=s), **bad})
+    with pytest.raises(CbsError):  # the output over the input
+        ops.int8_linear(x, torch.zeros(64, 64, dtype=I8, **dev), torch.zeros(64, **dev), out=x)
+    with pytest.raises(CbsError):
+        ops.int8_linear(torch.zeros(1, 131088, dtype=BF16, **dev), torch.zeros(1, 131088, dtype=I8, **dev), s[:1])
+
+    cache = ops.PagedCache.empty(4, 2, 16, 64)
+    k, slots = torch.zeros(3, 2, 64, dtype=BF16, **dev), torch.zeros(3, dtype=torch.int32, **dev)
+    with pytest.raises(ValueError):
+        ops.PagedCache(cache.k, cache.v, cache.k_scale[:3], cache.v_scale)
+    with pytest.raises(ValueError):
+        ops.PagedCache(k[None], k[None], cache.k_scale, cache.v_scale)
+    with pytest.raises(TypeError):
+        ops.PagedCache(cache.k, cache.v)
+    with pytest.raises(CbsError):  # a head dim that is no multiple of 8
+        ops.cache_read(ops.PagedCache.empty(4, 2, 16, 60), slots)
+    for bad in ((k.double(), k.double(), slots), (k, k.half(), slots), (k, k, slots.long())):
+        with pytest.raises(TypeError):
+            ops.cache_write(cache, *bad)
+    for bad in ((k[:2], k, slots), (k, k[:, :1], slots), (k.transpose(1, 2), k, slots), (k, k, slots[:2])):
+        with pytest.raises(ValueError):
+            ops.cache_write(cache, *bad)
+    with pytest.raises(TypeError):
+        ops.cache_read(cache, slots, torch.int8)
+
+    q = torch.zeros(3, 4, 64, dtype=BF16, **dev)
+    good = dict(q=q, cache=cache, table=torch.zeros(1, 2, dtype=torch.int32, **dev), starts=i32([0, 3]), lens=i32([5]))
+    ops.paged_attention(**good)
+    for bad in (dict(q=q.float()), dict(table=good["table"].long()), dict(lens=good["lens"].float()),
+                dict(cache=ops.PagedCache.empty(4, 2, 16, 64, F16)), dict(out=torch.zeros(3, 4, 64, **dev))):
+        with pytest.raises(TypeError):
+            ops.paged_attention(**{**good, **bad})
+    for bad in (dict(q=q[:, :3]), dict(q=q[:, :, :32]), dict(q=q.transpose(1, 2)), dict(starts=i32([0, 1, 3])),
+                dict(lens=i32([5, 5])), dict(window=-1), dict(table=good["table"][0]), dict(starts=good["starts"].cpu())):
+        with pytest.raises(ValueError):
+            ops.paged_attention(**{**good, **bad})
+    for bad in (dict(scale=math.nan), dict(scale=math.inf)):
+        with pytest.raises(CbsError):
+            ops.paged_attention(**{**good, **bad})
+    with pytest.raises(CbsError):  # dim 8: served by the cache, not by the attention
+        ops.paged_attention(**{**good, "q": torch.zeros(3, 4, 8, dtype=BF16, **dev),
+                               "cache": ops.PagedCache.empty(4, 2, 16, 8)})
+
+
+def test_served_block(ops):
+    """The example: chunks of prompts and single tokens through one block; its error is that of the 8-bit steps
+    (four layers and the cache, each near 1 / 254 of its rows' largest, some four times the root mean square)."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import served_block
+    assert served_block.main(["--width", "256", "--heads", "4", "--kv-heads", "2", "--prompts", "90", "1", "33",
+                              "--chunk", "32", "--decode", "6"]) < 0.05
