@@ -130,7 +130,7 @@ int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads
     // that: a workgroup needs some steps to fill its pipe.  The table's width is all that is
     // known of the lengths; where it leaves room for far more, larger chunks keep the
     // workgroups that find nothing to do below 16384.
-    const int64_t even = limit * pairs / (16 * num_cu) / 256 * 256, wide = round_up(limit * pairs / 16384, 256);
+    const int64_t even = limit * pairs / (16 * num_cu) / 256 * 256, wide = std::min<int64_t>(1 << 30, round_up(limit * pairs / 16384, 256));
     p.few.chunk = limit <= 1024 ? 1024 : (int)std::max(wide, std::min<int64_t>(2048, std::max<int64_t>(512, even)));
     p.few.chunks = (int)std::max<int64_t>(1, (limit + p.few.chunk - 1) / p.few.chunk);
 
