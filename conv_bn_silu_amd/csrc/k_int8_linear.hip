@@ -1,12 +1,19 @@
 // k_int8_linear.hip -- the product of the linear layer in 8-bit integers and its
 // epilogue: y[m][n] = act((sum_k a[m][k] w[n][k]) * sa[m] * sw[n] + bias[n]).
 //
-// Two kernels.  `linear_stream` is for few rows of x, where the layer is a read
-// of w: every wave takes the fragments of w straight from memory into the matrix
-// instruction, with no shared memory between, and the waves of a workgroup
-// divide K.  `linear_tile` is for many rows, where the matrix pipe is the
-// bound: tiles of both operands go through LDS.  The sums are 32-bit integers and
-// so the same whatever the order.
+// Three kernels.  `linear_stream` is for few tiles of output, where the layer is a
+// read of w: every wave takes the fragments of w straight from memory into the
+// matrix instruction, with no shared memory between, and the waves of a workgroup
+// divide K.  In `linear_ring` tiles of both operands go through LDS, with loads four steps
+// ahead, and `linear_tile` is the same for outputs that fill the CUs, where the matrix
+// pipe is the bound.  The sums are 32-bit integers and so the same whatever the order.
+//
+// Measured, us a call with the pass that quantises x (copying at 4.8 TB/s, matrix
+// products at 2.03 POP/s would take the second figure):
+//   1 x 4096 x 4096      stream     7.2   3.5      256 x 4096 x 4096     ring 64    16   4.4
+//   1 x 16384 x 4096     stream    14.7  14.0      1024 x 4096 x 4096    ring 128   30    17
+//   40 x 16384 x 4096    ring 64   17.0  14.3      4096 x 4096 x 4096    tile       76    68
+//   128 x 16384 x 4096   ring 64   21.2  15.1      8192 x 8192 x 8192    tile      525   541
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
