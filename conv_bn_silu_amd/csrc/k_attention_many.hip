@@ -322,27 +322,22 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                     if (!(((ahead >> key) & 1) && key <= last && key >= first)) s[i / 16][i % 16] = -INFINITY;
                 }
             }
-            float tops[4];
+            float tops[2] = {s[0][0], s[1][0]};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                tops[x] = fmaxf(s[x / 2][x % 2 * 8], s[x / 2][x % 2 * 8 + 1]);
+            for (int i = 1; i < 15; i += 2)
 #pragma unroll
-                for (int i = 2; i < 8; i += 2)
-                    tops[x] = fmaxf(fmaxf(tops[x], s[x / 2][x % 2 * 8 + i]), s[x / 2][x % 2 * 8 + i + 1]);
-            }
-            const float top = max_halves(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+                for (int kb = 0; kb < 2; ++kb) tops[kb] = fmaxf(fmaxf(tops[kb], s[kb][i]), s[kb][i + 1]);
+            const float top = max_halves(fmaxf(fmaxf(fmaxf(tops[0], s[0][15]), tops[1]), s[1][15]));
             const bool move = top > m && !((top - m) * qf <= kSlack);
-            float v_fade = 1.f;
-            if constexpr (S::kI8) {
-                const float ref = vrefs[buf];
-                if (ref != o_ref) v_fade = o_ref / ref, o_ref = ref;
-            }
-            if (__any(move) || v_fade != 1.f) {
+            float ref = o_ref;
+            if constexpr (S::kI8) ref = vrefs[buf];
+            if (__any(move || ref != o_ref)) {
                 const float now = move ? top : m;
                 const float fade = move ? (m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - now) * qf)) : 1.f;
                 m = now;
                 l *= fade;
-                const float both = fade * v_fade;
+                const float both = fade * (o_ref / ref);
+                o_ref = ref;
 #pragma unroll
                 for (int db = 0; db < NB; ++db) o[db] *= both;
             }
@@ -361,22 +356,27 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
             __builtin_amdgcn_sched_barrier(0);
             // a key that is not seen: 2^-inf = 0
             const float base = m == -INFINITY ? 0.f : m * qf;
-            X8 pr[4];
-            float sums[4] = {0.f, 0.f, 0.f, 0.f};
+            float sums[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 16][i % 16], qf, -base));
-                sums[i % 4] += w;
-                if constexpr (S::kI8) w *= per_key[i / 4][i % 4];
-                pr[i / 8][i % 8] = (X)w;
-            }
-            l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+            for (int t = 0; t < 4; ++t) {
+                X8 pr;
 #pragma unroll
-            for (int i = 0; i < 4 * NB; ++i) {
+                for (int i = 8 * t; i < 8 * t + 8; ++i) {
+                    float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 16][i % 16], qf, -base));
+                    sums[i % 2] += w;
+                    if constexpr (S::kI8) w *= per_key[i / 4][i % 4];
+                    pr[i % 8] = (X)w;
+                }
+                // these keys' matrix instructions run beside the next ones' exponentials
+#pragma unroll
+                for (int i = NB * t; i < NB * t + NB; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    o[i % NB] = mma32(ring[i % kAhead], pr, o[i % NB]);
+                    if (i + kAhead < 4 * NB) ring[i % kAhead] = read_v(i + kAhead);
+                }
                 __builtin_amdgcn_sched_barrier(0);
-                o[i % NB] = mma32(ring[i % kAhead], pr[i / NB], o[i % NB]);
-                if (i + kAhead < 4 * NB) ring[i % kAhead] = read_v(i + kAhead);
             }
+            l += sums[0] + sums[1];
             if (__builtin_expect(taken_out[buf] == j0, 0)) {
                 // what store() has taken out, to the rows that see it
 #pragma unroll 1
