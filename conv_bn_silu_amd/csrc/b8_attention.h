@@ -54,7 +54,7 @@ struct AttentionPlan {
 };
 hipError_t launch_attend_few(const AttentionPlan &p, hipStream_t st);
 hipError_t launch_attend_many(const AttentionPlan &p, hipStream_t st);
-int many_tile(int64_t dim);  // rows of its tile
+int many_tile(int64_t dim, bool int8);  // rows of its tile
 
 #ifdef __HIPCC__
 constexpr float kLog2e = 1.4426950408889634f;

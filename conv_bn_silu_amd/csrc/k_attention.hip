@@ -120,7 +120,9 @@ int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads
     // 32 rows only where the average sequence has more than 16: the registers they take cost
     // waves (8 sequences of 2 tokens, groups of 4, over 3000 keys: 41 us, with 16 rows 25)
     p.few.tile = dim <= 128 && tokens * group > 16 * batch ? 32 : 16;
-    p.many.tile = many_tile(dim);
+    // the chunks, and so the workspace, go by the tile of 8-bit caches, whatever this one is
+    const int64_t tile = many_tile(dim, true);
+    p.many.tile = many_tile(dim, p.a.cache.dtype == CBS_DTYPE_I8);
     // with no more tokens than sequences they are single tokens, as a rule
     p.few_only = tokens <= batch || tokens * group <= p.few.tile;
     p.slots = (int)(tokens * group / p.many.tile + std::min(batch, tokens * group / (p.few.tile + 1)));
@@ -138,7 +140,7 @@ int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads
     // workgroups than CUs, each of which holds one (512 tokens after 4000, 8 heads over 2: 162
     // workgroups 43 us, 252 40, 324 54).  Of the tiles that may be partial, half count.
     const int64_t partial = std::min(batch, tokens * group / (p.few.tile + 1));
-    const int64_t groups2 = std::max<int64_t>(1, (2 * tokens * group / p.many.tile + partial) * kv_heads);
+    const int64_t groups2 = std::max<int64_t>(1, (2 * tokens * group / tile + partial) * kv_heads);
     const int64_t want = limit <= 512 ? 1 : std::max<int64_t>(1, 2 * num_cu / groups2);
     p.many.chunk = want == 1 ? 1 << 30 : (int)std::max<int64_t>(256, round_up((limit + want - 1) / want, 64));
     p.many.chunks = want == 1 ? 1 : (int)std::max<int64_t>(1, (limit + p.many.chunk - 1) / p.many.chunk);

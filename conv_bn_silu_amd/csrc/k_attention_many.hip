@@ -20,7 +20,10 @@ constexpr int KT = 64;  // keys of a step
 // NB: dims in 32s.
 template <typename C, int NB> struct ManyShape {
     static constexpr bool kI8 = std::is_same_v<C, int8_t>;
-    static constexpr int kWaves = NB <= 4 ? 8 : 4;  // dim 256 needs the registers of two waves
+    // Dim 256 needs the registers of two waves; 16-bit caches at dim 64 need so few that three
+    // waves fit a SIMD (2 prompts of 6000: 8 waves 469 us, 12 waves 407; with 8-bit
+    // caches 543 and 593, for there it takes scratch memory or 168 registers of 196).
+    static constexpr int kWaves = NB > 4 ? 4 : NB == 2 && !kI8 ? 12 : 8;
     static constexpr int kThreads = 64 * kWaves, kTile = 32 * kWaves;
     static constexpr int kPitchDims = NB <= 2 ? 64 : NB <= 4 ? 128 : 256;
     static constexpr int kPitch = 2 * kPitchDims;                         // bytes of a row in LDS
@@ -478,7 +481,10 @@ template <typename T> hipError_t launch1(const AttentionPlan &p, hipStream_t st)
 
 }  // namespace
 
-int many_tile(int64_t dim) { return dim <= 128 ? ManyShape<int8_t, 4>::kTile : ManyShape<int8_t, 8>::kTile; }
+int many_tile(int64_t dim, bool int8) {
+    if (dim > 128) return ManyShape<int8_t, 8>::kTile;
+    return dim <= 64 && !int8 ? ManyShape<__bf16, 2>::kTile : ManyShape<int8_t, 4>::kTile;
+}
 
 hipError_t launch_attend_many(const AttentionPlan &p, hipStream_t st) {
     return p.a.dtype == CBS_DTYPE_BF16 ? launch1<__bf16>(p, st) : launch1<_Float16>(p, st);
