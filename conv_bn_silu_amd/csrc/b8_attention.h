@@ -43,18 +43,20 @@ namespace cbs {
 struct AttentionPart {
     int tile;           // rows of a tile
     int chunk, chunks;  // keys of a chunk; most chunks a tile can have
-    float *o, *ml;      // [line][chunk][dim] and [line][chunk][2]
+    int room;           // chunks that the workspace has room for
+    float *o, *ml;      // [line][room][dim] and [line][room][2]
 };
 struct AttentionPlan {
     AttentionArgs a;
     FastDiv page, group;
     bool few_only;  // attend_many does not run
+    bool split;     // attend_many: two waves to a row
     int slots;      // most tiles that attend_many can have
     AttentionPart few, many;
 };
 hipError_t launch_attend_few(const AttentionPlan &p, hipStream_t st);
 hipError_t launch_attend_many(const AttentionPlan &p, hipStream_t st);
-int many_tile(int64_t dim, bool int8);  // rows of its tile
+int many_tile(int64_t dim, bool int8, bool split);  // rows of its tile
 
 #ifdef __HIPCC__
 constexpr float kLog2e = 1.4426950408889634f;

@@ -17,7 +17,7 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;
 template <typename T, int ND>
 __device__ __forceinline__ void join_dims(const AttentionPlan &p, const AttentionPart &part, int64_t line, int n, int64_t out) {
     const int lane = (int)threadIdx.x % 64, dim = p.a.cache.dim;
-    const float *ml = part.ml + 2 * line * part.chunks, *o = part.o + line * part.chunks * dim;
+    const float *ml = part.ml + 2 * line * part.room, *o = part.o + line * part.room * dim;
     float top = -INFINITY;
     for (int c = lane; c < n; c += 64) top = fmaxf(top, ml[2 * c]);
 #pragma unroll
@@ -106,11 +106,11 @@ template <typename T> __global__ __launch_bounds__(kThreads) void join_parts(con
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // Lays a kernel's parts out in the workspace, `at` floats of which are taken.
 void place_parts(AttentionPart &part, float *ws, int64_t &at, int64_t lines, int64_t dim) {
-    if (part.chunks <= 1) return;
+    if (part.room <= 1) return;
     part.o = ws + at;
-    at += lines * part.chunks * dim;
+    at += lines * part.room * dim;
     part.ml = ws + at;
-    at += lines * part.chunks * 2;
+    at += lines * part.room * 2;
 }
 
 // The division of a call; returns the bytes of workspace that it takes.
@@ -120,12 +120,18 @@ int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads
     // 32 rows only where the average sequence has more than 16: the registers they take cost
     // waves (8 sequences of 2 tokens, groups of 4, over 3000 keys: 41 us, with 16 rows 25)
     p.few.tile = dim <= 128 && tokens * group > 16 * batch ? 32 : 16;
-    // the chunks, and so the workspace, go by the tile of 8-bit caches, whatever this one is
-    const int64_t tile = many_tile(dim, true);
-    p.many.tile = many_tile(dim, p.a.cache.dtype == CBS_DTYPE_I8);
     // with no more tokens than sequences they are single tokens, as a rule
     p.few_only = tokens <= batch || tokens * group <= p.few.tile;
-    p.slots = (int)(tokens * group / p.many.tile + std::min(batch, tokens * group / (p.few.tile + 1)));
+    // Two waves to a row where tiles of 256 rows leave CUs idle and a tile's keys are not many times
+    // its tokens (then chunks fill the CUs as well).  One and two, us: a prompt of 1000 49.4 and
+    // 36.0, of 2000 85.1 and 73.0, of 4000 167 and 211; 512 tokens after 4000 36.4 and 38.5.  In
+    // between it goes both ways: three of 200 to 900 after up to 3000, 15 heads over 3, 73 and 62;
+    // 2000 after 8000, 4 heads over 1, 72.5 and 77.9.
+    const int64_t partial = std::min(batch, tokens * group / (p.few.tile + 1));
+    const int64_t keys = p.a.window ? std::min(limit, p.a.window + tokens / std::max<int64_t>(1, batch)) : limit;
+    p.split = dim <= 128 && (2 * tokens * group / many_tile(dim, true, false) + partial) * kv_heads < 2 * num_cu && keys * batch <= 8 * tokens;
+    p.many.tile = many_tile(dim, p.a.cache.dtype == CBS_DTYPE_I8, p.split);
+    p.slots = (int)(tokens * group / p.many.tile + partial);
 
     // attend_few: 1024 keys are soon read, and joining chunks takes a kernel more.  Beyond,
     // so many chunks that every CU has several workgroups to its name, but no more than
@@ -134,16 +140,22 @@ int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads
     // workgroups that find nothing to do below 16384.
     const int64_t even = limit * pairs / (16 * num_cu) / 256 * 256, wide = std::min<int64_t>(1 << 30, round_up(limit * pairs / 16384, 256));
     p.few.chunk = limit <= 1024 ? 1024 : (int)std::max(wide, std::min<int64_t>(2048, std::max<int64_t>(512, even)));
-    p.few.chunks = (int)std::max<int64_t>(1, (limit + p.few.chunk - 1) / p.few.chunk);
+    p.few.chunks = p.few.room = (int)std::max<int64_t>(1, (limit + p.few.chunk - 1) / p.few.chunk);
 
     // attend_many: chunks only where there are too few tiles for the CUs, and no more
     // workgroups than CUs, each of which holds one (512 tokens after 4000, 8 heads over 2: 162
     // workgroups 43 us, 252 40, 324 54).  Of the tiles that may be partial, half count.
-    const int64_t partial = std::min(batch, tokens * group / (p.few.tile + 1));
-    const int64_t groups2 = std::max<int64_t>(1, (2 * tokens * group / tile + partial) * kv_heads);
-    const int64_t want = limit <= 512 ? 1 : std::max<int64_t>(1, 2 * num_cu / groups2);
-    p.many.chunk = want == 1 ? 1 << 30 : (int)std::max<int64_t>(256, round_up((limit + want - 1) / want, 64));
-    p.many.chunks = want == 1 ? 1 : (int)std::max<int64_t>(1, (limit + p.many.chunk - 1) / p.many.chunk);
+    // The workspace has room for the chunks of either form (it is asked for without the window),
+    // by the tiles of 8-bit caches.
+    p.many.room = 1;
+    for (int split = dim <= 128; split >= 0; --split) {
+        const int64_t groups2 = std::max<int64_t>(1, (2 * tokens * group / many_tile(dim, true, split) + partial) * kv_heads);
+        const int64_t want = limit <= 512 ? 1 : std::max<int64_t>(1, 2 * num_cu / groups2);
+        const int chunk = want == 1 ? 1 << 30 : (int)std::max<int64_t>(256, round_up((limit + want - 1) / want, 64));
+        const int chunks = want == 1 ? 1 : (int)std::max<int64_t>(1, (limit + chunk - 1) / chunk);
+        p.many.room = std::max(p.many.room, chunks);
+        if (split == (int)p.split) p.many.chunk = chunk, p.many.chunks = chunks;
+    }
 
     int64_t at = 0;
     place_parts(p.few, ws, at, p.few_only ? tokens * heads : pairs * p.few.tile, dim);

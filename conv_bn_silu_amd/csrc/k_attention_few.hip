@@ -387,7 +387,7 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
             if (n_chunks == 1) {
                 Value<T>::store1((T *)a.out + out_line(p, seq, kvh, r0 + row) * dim + d, divide(out, sum));
             } else {
-                const int64_t line = few_line(p, seq, kvh, r0 + row) * p.few.chunks + c;
+                const int64_t line = few_line(p, seq, kvh, r0 + row) * p.few.room + c;
                 p.few.o[line * dim + d] = out;
                 if (d == 0) p.few.ml[2 * line] = top, p.few.ml[2 * line + 1] = sum;
             }

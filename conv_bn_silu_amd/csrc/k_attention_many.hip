@@ -15,26 +15,32 @@
 namespace cbs {
 namespace {
 
-constexpr int KT = 64;  // keys of a step
+constexpr int KT = 64;  // keys of a wave's step
 
-// NB: dims in 32s.
-template <typename C, int NB> struct ManyShape {
+// NB: dims in 32s.  SPLIT 2: half of the waves have the same rows as the other half and
+// take every second 64 keys; the two meet at the end.  A tile has half of the rows then,
+// and half of the steps in a row, for more bytes through LDS a row (a prompt of 1000, 32 heads
+// over 8, 49.4 -> 36.0 us; of 4000, which fills the CUs without it, 167 and 211).
+template <typename C, int NB, int SPLIT> struct ManyShape {
     static constexpr bool kI8 = std::is_same_v<C, int8_t>;
     // Dim 256 needs the registers of two waves; 16-bit caches at dim 64 need so few that three
     // waves fit a SIMD (2 prompts of 6000: 8 waves 469 us, 12 waves 407; with 8-bit
     // caches 543 and 593, for there it takes scratch memory or 168 registers of 196).
-    static constexpr int kWaves = NB > 4 ? 4 : NB == 2 && !kI8 ? 12 : 8;
-    static constexpr int kThreads = 64 * kWaves, kTile = 32 * kWaves;
+    static constexpr int kWaves = NB > 4 ? 4 : NB == 2 && !kI8 && SPLIT == 1 ? 12 : 8;
+    static constexpr int kGroups = kWaves / SPLIT;  // waves with rows of their own
+    static constexpr int kThreads = 64 * kWaves, kTile = 32 * kGroups, KS = KT * SPLIT;
     static constexpr int kPitchDims = NB <= 2 ? 64 : NB <= 4 ? 128 : 256;
     static constexpr int kPitch = 2 * kPitchDims;                         // bytes of a row in LDS
     static constexpr int kPieces = kPitchDims * (int)sizeof(C) / 16;      // 16-byte pieces of a row of the cache
     static constexpr int kRowsPerLoad = kThreads / kPieces;
-    static constexpr int kLoads = kRowsPerLoad < KT ? KT / kRowsPerLoad : 1;
-    static constexpr bool kIdle = kRowsPerLoad > KT;                      // threads without a piece
-    static constexpr int kSide = KT * kPitch;                             // bytes of keys, or of values
+    static constexpr int kLoads = kRowsPerLoad < KS ? KS / kRowsPerLoad : 1;
+    static constexpr bool kIdle = kRowsPerLoad > KS;                      // threads without a piece
+    static constexpr int kSide = KS * kPitch;                             // bytes of keys, or of values
     static constexpr int kOutPitch = kPitch + 16;
     static constexpr int kOutBytes = kTile * kOutPitch;
+    static constexpr int kMeet = NB * 4096 + 512;  // bytes of a wave's outputs, maxima and sums
     static constexpr int kBytes = 4 * kSide > kOutBytes ? 4 * kSide : kOutBytes;
+    static_assert(SPLIT == 1 || kGroups * kMeet <= kBytes, "");
     // Pieces of a row are exchanged: a read of keys takes the same dims of 16 rows at a
     // time, a transposed read of values 32 dims of 4 rows.
     static __device__ __forceinline__ int swap_k(int row) { return NB <= 2 ? (row >> 1) & 7 : row & 15; }
@@ -93,19 +99,21 @@ template <typename X> __device__ __forceinline__ bool take_out(u32x4 &v) {
     return any;
 }
 
-template <typename T, typename C, int NB>
-__global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kWaves / 4)) void attend_many(const AttentionPlan p) {
-    using S = ManyShape<C, NB>;
+template <typename T, typename C, int NB, int SPLIT>
+__global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, NB, SPLIT>::kWaves / 4)) void attend_many(const AttentionPlan p) {
+    using S = ManyShape<C, NB, SPLIT>;
+    constexpr int KS = S::KS;
     using X8 = typename Operand<T, C>::x8;
     using X = typename Operand<T, C>::type;
     constexpr int kSteps = 2 * NB, kAhead = 4;
     __shared__ __attribute__((aligned(16))) unsigned char lds[S::kBytes];
-    __shared__ __attribute__((aligned(16))) float kscale[2][KT], vscale[2][KT];
-    __shared__ uint64_t valid_bits[2];
-    __shared__ float vrefs[2];
-    __shared__ int taken_out[2];  // the last step in whose values store() found something to take out
+    __shared__ __attribute__((aligned(16))) float kscale[2][KS], vscale[2][KS];
+    __shared__ uint64_t valid_bits[2][SPLIT];
+    __shared__ float vrefs[2][SPLIT];
+    __shared__ int taken_out[2][SPLIT];  // the last step in whose values store() found something to take out
     const AttentionArgs &a = p.a;
     const int tid = (int)threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int group = wave % S::kGroups, part = wave / S::kGroups;  // its rows, its keys of a step
     const int col = lane % 32, half = lane / 32;
     const int hk = a.cache.heads, dim = a.cache.dim;
     // the key/value head is innermost: with 8 of them each XCD's L2 serves one
@@ -122,7 +130,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     const int lo = keys.lo + c * p.many.chunk, hi = min(keys.hi, lo + p.many.chunk);
     const int old = seq.len - seq.n;
     // this wave's rows
-    const int w0 = min(r0 + 32 * wave, r1 - 1), w1 = min(r0 + 32 * wave + 31, r1 - 1);
+    const int w0 = min(r0 + 32 * group, r1 - 1), w1 = min(r0 + 32 * group + 31, r1 - 1);
     const int wave_min = old + (int)p.group.div((uint32_t)w0), wave_max = old + (int)p.group.div((uint32_t)w1);
     const int wave_low = first_key(p, wave_min), wave_high_low = first_key(p, wave_max);
 
@@ -130,7 +138,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     const C *const kdata = (const C *)a.cache.k, *const vdata = (const C *)a.cache.v;
 
     // this lane's row
-    const int r = min(r0 + 32 * wave + col, r1 - 1), tok = (int)p.group.div((uint32_t)r);
+    const int r = min(r0 + 32 * group + col, r1 - 1), tok = (int)p.group.div((uint32_t)r);
     const int pos = old + tok, low = first_key(p, pos);
     float qf = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-149f);  // above zero, so that -inf stays what it is
     X8 q[kSteps];
@@ -169,8 +177,8 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
 
     // Staging: thread's piece of rows my_row, my_row + kRowsPerLoad, ...; the first wave
     // also looks after the keys as such, one a lane: whether they are there, their scales.
-    const bool my_part = !S::kIdle || tid / S::kPieces < KT;
-    const int my_row = tid / S::kPieces % KT, my_d = tid % S::kPieces * (16 / (int)sizeof(C));
+    const bool my_part = !S::kIdle || tid / S::kPieces < KS;
+    const int my_row = tid / S::kPieces % KS, my_d = tid % S::kPieces * (16 / (int)sizeof(C));
     const bool my_dims = my_d < dim;
     u32x4 kreg[S::kLoads], vreg[S::kLoads];
     bool vok[S::kLoads];
@@ -186,7 +194,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     auto look_up = [&](int j0) {
 #pragma unroll
         for (int i = 0; i < S::kLoads; ++i) next_page[i] = page_of(j0 + my_row + i * S::kRowsPerLoad);
-        if (wave == 0) key_page = page_of(j0 + lane);
+        if (group == 0) key_page = page_of(j0 + KT * part + lane);
     };
     auto load = [&](int j0) {
 #pragma unroll
@@ -195,9 +203,9 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
             kreg[i] = *(const u32x4 *)(kdata + at);
             vreg[i] = *(const u32x4 *)(vdata + at);
         }
-        if (wave == 0) {
+        if (group == 0) {
             bool ok;
-            const int64_t row = row_of(j0 + lane, key_page, ok);
+            const int64_t row = row_of(j0 + KT * part + lane, key_page, ok);
             key_bits = __ballot(ok);
             if constexpr (S::kI8) {
                 ks = a.cache.k_scale[row];
@@ -212,7 +220,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     const int tile_low = first_key(p, old + (int)p.group.div((uint32_t)(r1 - 1)));
     auto store = [&](int buf, int j0) {
         unsigned char *const kbuf = lds + buf * 2 * S::kSide, *const vbuf = kbuf + S::kSide;
-        const bool part = j0 + KT - 1 > tile_min || j0 < tile_low;
+        const bool shared = j0 + KS - 1 > tile_min || j0 < tile_low;
         bool odd = false;
 #pragma unroll
         for (int i = 0; i < S::kLoads; ++i) {
@@ -233,20 +241,20 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                 // past dim q is zero, and a key's infinity or NaN has no place there
                 const uint32_t kkeep = my_dims ? ~0u : 0u, vkeep = vok[i] ? ~0u : 0u;
                 u32x4 v = vreg[i] & vkeep;
-                if (part) odd |= take_out<X>(v);
+                if (shared) odd |= take_out<X>(v);
                 *(u32x4 *)(kbuf + row * S::kPitch + ((piece ^ S::swap_k(row)) * 16)) = k & kkeep;
                 *(u32x4 *)(vbuf + row * S::kPitch + ((piece ^ S::swap_v(row)) * 16)) = v;
             }
         }
         if constexpr (!S::kI8) {
-            if (__any(odd) && lane == 0) taken_out[buf] = j0;
+            if (__any(odd) && lane < SPLIT) taken_out[buf][lane] = j0;
         }
-        if (wave == 0) {
+        if (group == 0) {
             if constexpr (S::kI8) {
                 const uint32_t bits = magnitude(vs);
                 const bool there = (key_bits >> lane) & 1, counts = there && bits < 0x7F800000u;
                 const uint64_t taken = __ballot(there && !counts);
-                if (taken && lane == 0) taken_out[buf] = j0;
+                if (taken && lane == 0) taken_out[buf][part] = j0;
                 if (!counts) vs = 0.f;
                 if (__any(vs > vref)) {
                     uint32_t top = counts ? bits : 0u;
@@ -254,11 +262,11 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                     for (int x = 1; x < 64; x *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, x, 64));
                     vref = power_above(top);
                 }
-                kscale[buf][lane] = finite_or_nan(ks);
-                vscale[buf][lane] = vs * (1.f / vref);
-                if (lane == 0) vrefs[buf] = vref;
+                kscale[buf][KT * part + lane] = finite_or_nan(ks);
+                vscale[buf][KT * part + lane] = vs * (1.f / vref);
+                if (lane == 0) vrefs[buf][part] = vref;
             }
-            if (lane == 0) valid_bits[buf] = key_bits;
+            if (lane == 0) valid_bits[buf][part] = key_bits;
         }
     };
 
@@ -269,27 +277,28 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     f32x16 o[NB] = {};
     float m = -INFINITY, l = 0.f, o_ref = 0x1p-126f;
 
-    if (tid < 2) taken_out[tid] = -1;
+    if (tid < 2 * SPLIT) taken_out[tid / SPLIT][tid % SPLIT] = -1;
     __syncthreads();
     if (lo < hi) {
         look_up(lo);
         load(lo);
-        look_up(lo + KT);
+        look_up(lo + KS);
         store(0, lo);
     }
     int buf = 0;
-    for (int j0 = lo; j0 < hi; j0 += KT, buf ^= 1) {
+    for (int j0 = lo; j0 < hi; j0 += KS, buf ^= 1) {
         __syncthreads();
-        const bool more = j0 + KT < hi;
+        const bool more = j0 + KS < hi;
+        const int jw = j0 + KT * part;
         if (more) {
-            load(j0 + KT);
-            if (j0 + 2 * KT < hi) look_up(j0 + 2 * KT);
+            load(j0 + KS);
+            if (j0 + 2 * KS < hi) look_up(j0 + 2 * KS);
         }
-        if (j0 <= wave_max && j0 + KT > wave_low) {
+        if (jw < hi && jw <= wave_max && jw + KT > wave_low) {
             // An operand's piece number is exchanged by exclusive or, and so is its byte: one
             // operation for a step of the scores or a block of the outputs, and the rest is
             // the instruction's offset.
-            int k_at = buf * 2 * S::kSide + k_lane, v_at = buf * 2 * S::kSide + S::kSide + v_lane;
+            int k_at = buf * 2 * S::kSide + part * KT * S::kPitch + k_lane, v_at = k_at - k_lane + S::kSide + v_lane;
             asm volatile("" : "+v"(k_at), "+v"(v_at));  // made anew for each step, or each costs a register
             // Fragments are read kAhead matrix instructions before their use, and the order is
             // held: left alone the compiler reads each just before it is wanted, and waits.
@@ -304,21 +313,21 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                 s[i % 2] = mma32(ring[i % kAhead], q[i / 2], i < 2 ? f32x16{} : s[i % 2]);
                 if (i + kAhead < 2 * kSteps) ring[i % kAhead] = read_k(i + kAhead);
             }
-            const uint64_t valid = valid_bits[buf];
+            const uint64_t valid = valid_bits[buf][part];
             // the lane's keys are 32 kb + 8 g + 4 half + 0..3
             f32x4 per_key[8];
             if constexpr (S::kI8) {
 #pragma unroll
-                for (int g = 0; g < 8; ++g) per_key[g] = *(const f32x4 *)(&kscale[buf][8 * g + 4 * half]);
+                for (int g = 0; g < 8; ++g) per_key[g] = *(const f32x4 *)(&kscale[buf][KT * part + 8 * g + 4 * half]);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[i / 16][i % 16] *= per_key[i / 4][i % 4];
             }
-            if (!(valid == ~0ull && j0 + KT - 1 <= wave_min && j0 >= wave_high_low)) {
+            if (!(valid == ~0ull && jw + KT - 1 <= wave_min && jw >= wave_high_low)) {
                 int my_half = half;
                 asm volatile("" : "+v"(my_half));
                 const uint64_t ahead = valid >> (4 * my_half);
-                const int last = pos - j0 - 4 * my_half, first = low - j0 - 4 * my_half;
+                const int last = pos - jw - 4 * my_half, first = low - jw - 4 * my_half;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int key = 32 * (i / 16) + 8 * (i % 16 / 4) + i % 4;  // less 4 half
@@ -333,7 +342,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
             const float top = max_halves(fmaxf(fmaxf(fmaxf(tops[0], s[0][15]), tops[1]), s[1][15]));
             const bool move = top > m && !((top - m) * qf <= kSlack);
             float ref = o_ref;
-            if constexpr (S::kI8) ref = vrefs[buf];
+            if constexpr (S::kI8) ref = vrefs[buf][part];
             if (__any(move || ref != o_ref)) {
                 const float now = move ? top : m;
                 const float fade = move ? (m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - now) * qf)) : 1.f;
@@ -346,7 +355,7 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
             }
             if constexpr (S::kI8) {
 #pragma unroll
-                for (int g = 0; g < 8; ++g) per_key[g] = *(const f32x4 *)(&vscale[buf][8 * g + 4 * half]);
+                for (int g = 0; g < 8; ++g) per_key[g] = *(const f32x4 *)(&vscale[buf][KT * part + 8 * g + 4 * half]);
             }
             // values: keys 16 t + 4 half + 0..3 and 8 above those, of dim 32 db + col
             auto read_v = [&](int i) {
@@ -380,10 +389,10 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                 __builtin_amdgcn_sched_barrier(0);
             }
             l += sums[0] + sums[1];
-            if (__builtin_expect(taken_out[buf] == j0, 0)) {
+            if (__builtin_expect(taken_out[buf][part] == j0, 0)) {
                 // what store() has taken out, to the rows that see it
 #pragma unroll 1
-                for (int j = j0; j < min(hi, j0 + KT); ++j) {
+                for (int j = jw; j < min(hi, jw + KT); ++j) {
                     bool there;
                     const int64_t row = row_of(j, table[p.page.div((uint32_t)j)], there);
                     const bool sees = there && j <= pos && j >= low;
@@ -406,16 +415,45 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
                 }
             }
         }
-        if (more) store(buf ^ 1, j0 + KT);
+        if (more) store(buf ^ 1, j0 + KS);
     }
 
     // the lane has one row, of every 32 dims 16
+    float ref = S::kI8 ? o_ref : 1.f, top = m == -INFINITY ? -INFINITY : m * qf;  // units of the outputs and exponents
+    if constexpr (SPLIT == 2) {
+        // the second half of the waves hand theirs over, lane by lane
+        __syncthreads();
+        float *const meet = (float *)(lds + group * S::kMeet), *const meet_ml = meet + NB * 1024;
+        if (part == 1) {
+#pragma unroll
+            for (int x = 0; x < 4 * NB; ++x) {
+                const f32x4 v = {o[x / 4][x % 4 * 4], o[x / 4][x % 4 * 4 + 1], o[x / 4][x % 4 * 4 + 2], o[x / 4][x % 4 * 4 + 3]};
+                *(f32x4 *)(meet + (x * 64 + lane) * 4) = v * ref;
+            }
+            meet_ml[lane] = top, meet_ml[64 + lane] = l;
+        }
+        __syncthreads();
+        if (part == 0) {
+            const float other = meet_ml[lane], both_top = fmaxf(top, other);
+            const float mine = top == both_top ? 1.f : __builtin_amdgcn_exp2f(top - both_top);
+            const float theirs = other == both_top ? 1.f : __builtin_amdgcn_exp2f(other - both_top);
+            l = l * mine + meet_ml[64 + lane] * theirs;
+            const float scale = mine * ref;
+#pragma unroll
+            for (int x = 0; x < 4 * NB; ++x) {
+                const f32x4 v = *(const f32x4 *)(meet + (x * 64 + lane) * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x / 4][x % 4 * 4 + e] = o[x / 4][x % 4 * 4 + e] * scale + v[e] * theirs;
+            }
+            ref = 1.f, top = both_top;
+        }
+    }
     const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     const float sum = __uint_as_float(both[0]) + __uint_as_float(both[1]);
     // Through LDS, so that a row's dims are stored side by side; parts, in fp32, half of them at a time.
     __syncthreads();
-    unsigned char *const stage = lds + wave * 32 * S::kOutPitch;
-    const float ref = S::kI8 ? o_ref : 1.f;
+    if (part != 0) return;
+    unsigned char *const stage = lds + group * 32 * S::kOutPitch;
     constexpr int kOutPieces = S::kPitch / 16;
     if (n_chunks > 1) {
         constexpr int kHalf = S::kPitchDims / 2;
@@ -432,17 +470,17 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
             __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
             for (int i = lane; i < 32 * kOutPieces; i += 64) {
-                const int row = i / kOutPieces, d = h * kHalf + i % kOutPieces * 4, at = r0 + 32 * wave + row;
+                const int row = i / kOutPieces, d = h * kHalf + i % kOutPieces * 4, at = r0 + 32 * group + row;
                 if (at < r1 && d < dim)
-                    *(f32x4 *)(p.many.o + (out_line(p, seq, kvh, at) * p.many.chunks + c) * dim + d) =
+                    *(f32x4 *)(p.many.o + (out_line(p, seq, kvh, at) * p.many.room + c) * dim + d) =
                         *(const f32x4 *)(stage + row * S::kOutPitch + i % kOutPieces * 16);
             }
             __builtin_amdgcn_wave_barrier();
         }
-        const int mine = r0 + 32 * wave + col;
+        const int mine = r0 + 32 * group + col;
         if (half == 0 && mine < r1) {
-            const int64_t line = out_line(p, seq, kvh, mine) * p.many.chunks + c;
-            p.many.ml[2 * line] = m == -INFINITY ? -INFINITY : m * qf, p.many.ml[2 * line + 1] = sum;
+            const int64_t line = out_line(p, seq, kvh, mine) * p.many.room + c;
+            p.many.ml[2 * line] = top, p.many.ml[2 * line + 1] = sum;
         }
         return;
     }
@@ -459,21 +497,24 @@ __global__ __launch_bounds__((ManyShape<C, NB>::kThreads), (ManyShape<C, NB>::kW
     __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
     for (int i = lane; i < 32 * kOutPieces; i += 64) {
-        const int row = i / kOutPieces, d = i % kOutPieces * 8, at = r0 + 32 * wave + row;
+        const int row = i / kOutPieces, d = i % kOutPieces * 8, at = r0 + 32 * group + row;
         if (at < r1 && d < dim)
             ((Any16 *)((T *)a.out + out_line(p, seq, kvh, at) * dim + d))->v = *(const u32x4 *)(stage + row * S::kOutPitch + 2 * d);
     }
 }
 
-template <typename T, typename C, int NB> hipError_t launch3(const AttentionPlan &p, hipStream_t st) {
+template <typename T, typename C, int NB, int SPLIT> hipError_t launch4(const AttentionPlan &p, hipStream_t st) {
     const int64_t grid = (int64_t)p.slots * p.many.chunks * p.a.cache.heads;
-    attend_many<T, C, NB><<<(unsigned)grid, ManyShape<C, NB>::kThreads, 0, st>>>(p);
+    attend_many<T, C, NB, SPLIT><<<(unsigned)grid, ManyShape<C, NB, SPLIT>::kThreads, 0, st>>>(p);
     return hipGetLastError();
+}
+template <typename T, typename C, int NB> hipError_t launch3(const AttentionPlan &p, hipStream_t st) {
+    return p.split ? launch4<T, C, NB, 2>(p, st) : launch4<T, C, NB, 1>(p, st);
 }
 template <typename T, typename C> hipError_t launch2(const AttentionPlan &p, hipStream_t st) {
     if (p.a.cache.dim <= 64) return launch3<T, C, 2>(p, st);
     if (p.a.cache.dim <= 96) return launch3<T, C, 3>(p, st);
-    return p.a.cache.dim <= 128 ? launch3<T, C, 4>(p, st) : launch3<T, C, 8>(p, st);
+    return p.a.cache.dim <= 128 ? launch3<T, C, 4>(p, st) : launch4<T, C, 8, 1>(p, st);
 }
 template <typename T> hipError_t launch1(const AttentionPlan &p, hipStream_t st) {
     return p.a.cache.dtype == CBS_DTYPE_I8 ? launch2<T, int8_t>(p, st) : launch2<T, T>(p, st);
@@ -481,9 +522,10 @@ template <typename T> hipError_t launch1(const AttentionPlan &p, hipStream_t st)
 
 }  // namespace
 
-int many_tile(int64_t dim, bool int8) {
-    if (dim > 128) return ManyShape<int8_t, 8>::kTile;
-    return dim <= 64 && !int8 ? ManyShape<__bf16, 2>::kTile : ManyShape<int8_t, 4>::kTile;
+int many_tile(int64_t dim, bool int8, bool split) {
+    if (dim > 128) return ManyShape<int8_t, 8, 1>::kTile;
+    if (split) return ManyShape<int8_t, 4, 2>::kTile;
+    return dim <= 64 && !int8 ? ManyShape<__bf16, 2, 1>::kTile : ManyShape<int8_t, 4, 1>::kTile;
 }
 
 hipError_t launch_attend_many(const AttentionPlan &p, hipStream_t st) {

@@ -538,6 +538,18 @@ def test_attention_dims(ops, dim):
             check_case(ops, c, f"dim {dim} {new} {types}")
 
 
+@pytest.mark.parametrize("types", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("new,lens,heads,hk,dim,window",
+                         [([700], [700], 8, 2, 128, 0), ([1000, 90, 600], [1000, 700, 1500], 4, 1, 64, 0),
+                          ([400], [5000], 4, 2, 80, 300), ([300, 40], [2000, 3000], 6, 3, 128, 130),
+                          ([129, 64, 5], [129, 600, 700], 2, 1, 96, 0)],
+                         ids=["prompt", "prompts", "window", "windows", "ragged"])
+def test_attention_prompts(ops, new, lens, heads, hk, dim, window, types):
+    """Prompts that are too short to fill the CUs with whole tiles, with and without chunks."""
+    c = attention_case(new, lens, heads, hk, dim, 16, *types, window=window, seed=37)
+    check_case(ops, c, f"{new} {lens} {dim} {window} {types}")
+
+
 @pytest.mark.parametrize("new,lens", [([1, 1], [900, 40]), ([5, 9], [600, 9]), ([80, 300], [500, 300])],
                          ids=["decode", "few", "chunk"])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
