@@ -20,8 +20,9 @@ struct CodesLayout {
     int64_t bytes;
 };
 CodesLayout codes_layout(void *workspace, int64_t M, int64_t K);
-// Quantises x; with `to`, also lays the rows of w out there, Kp apart.
-hipError_t launch_quant_rows(const LinearArgs &a, const CodesLayout &l, int8_t *to, hipStream_t st);
+// Quantises x; with `to`, also lays the rows of w out there, Kp apart; with `zeros`, also
+// clears `count` numbers there.
+hipError_t launch_quant_rows(const LinearArgs &a, const CodesLayout &l, int8_t *to, int *zeros, int count, hipStream_t st);
 
 #ifdef __HIPCC__
 // 16 bytes of w at byte `at`, some or all of which may lie past its `size` bytes: those

@@ -6,7 +6,8 @@
 // matrix instruction, with no shared memory between, and the waves of a workgroup
 // divide K.  In `linear_ring` tiles of both operands go through LDS, with loads four steps
 // ahead, and `linear_tile` is the same for outputs that fill the CUs, where the matrix
-// pipe is the bound.  The sums are 32-bit integers and so the same whatever the order.
+// pipe is the bound.  The sums are 32-bit integers and so the same whatever the order; where
+// few tiles have long sums, several workgroups of linear_ring divide a tile's K.
 //
 // Measured, us a call with the pass that quantises x (copying at 4.8 TB/s, matrix
 // products at 2.03 POP/s would take the second figure):
@@ -14,8 +15,10 @@
 //   1 x 16384 x 4096     stream    14.7  14.0      1024 x 4096 x 4096    ring 128   30    17
 //   40 x 16384 x 4096    ring 64   17.0  14.3      4096 x 4096 x 4096    tile       76    68
 //   128 x 16384 x 4096   ring 64   21.2  15.1      8192 x 8192 x 8192    tile      525   541
+//   128 x 1024 x 8192    4 parts   16.7   2.2
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "b8_device.h"
@@ -216,6 +219,10 @@ struct TileParams {
     const float *w_scale, *bias;
     void *y;
     int M, N, m_tiles, n_tiles;
+    // linear_ring, K divided between `splits` workgroups: their sums, [split][tile][wave][32][64] in
+    // the order of the registers, and how many of a tile's are there
+    int splits, split_steps;
+    int *sums, *arrived;
 };
 
 // Stores a wave's sums, 32 MB x 64 of them from (m0, n0).  A lane holds one n and, of every
@@ -317,9 +324,10 @@ struct Loads {
     uint32_t off_a[kLoads], off_b[kLoads], size_a, size_b;
     int64_t step_a;
     int wave, steps;
-    __device__ __forceinline__ Loads(const TileParams &p, int m0, int n0, int bn, int w, int lane) {
+    // The steps [s0, s0 + n) of K.
+    __device__ __forceinline__ Loads(const TileParams &p, int m0, int n0, int bn, int w, int lane, int s0, int n) {
         const uint32_t block = (uint32_t)p.l.rows * 64;
-        wave = w, steps = p.l.Kp / 128;
+        wave = w, steps = n;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int r = (wave * kLoads + i) * 8 + lane / 8, c = (lane % 8) ^ ((r >> 1) & 7);
@@ -330,9 +338,9 @@ struct Loads {
             const int r = (wave * kLoads + i) * 8 + lane / 8, c = (lane % 8) ^ ((r >> 1) & 7);
             off_b[i] = (uint32_t)(r * p.w_stride + c * 16);
         }
-        base_a = p.l.codes + (int64_t)m0 * 64, base_b = p.w + (int64_t)n0 * p.w_stride;
         step_a = 2 * (int64_t)block;
-        size_a = 2 * block - (uint32_t)m0 * 64, size_b = (uint32_t)(min(bn, p.N - n0) * p.w_stride);
+        base_a = p.l.codes + (int64_t)m0 * 64 + s0 * step_a, base_b = p.w + (int64_t)n0 * p.w_stride + s0 * 128;
+        size_a = 2 * block - (uint32_t)m0 * 64, size_b = (uint32_t)(min(bn, p.N - n0) * p.w_stride) - (uint32_t)s0 * 128;
     }
     // A step's part of the operands, and its size.
     __device__ __forceinline__ const int8_t *a_at(int s) const { return base_a + s * step_a; }
@@ -353,7 +361,7 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64), 2) void linear_t
     const int lane = (int)threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
     const Tile t = place((int)blockIdx.x, p.m_tiles, p.n_tiles);
     const int m0 = t.m * BM, n0 = t.n * BN;
-    const Loads loads(p, m0, n0, BN, wave, lane);
+    const Loads loads(p, m0, n0, BN, wave, lane, 0, p.l.Kp / 128);
     const int wm = wave / kWavesN * 32 * MB, wn = wave % kWavesN * 64, r32 = lane % 32, half = lane / 32;
     const int swap = (r32 >> 1) & 7;  // the same for every 32 rows
     const int at_a = (wm + r32) * 128, at_b = (wn + r32) * 128;
@@ -381,6 +389,43 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64), 2) void linear_t
     store_sums<T, SILU, MB>(p, acc, (int *)(mine + wave % kEach * kTileBytes), m0 + wm, n0 + wn);
 }
 
+// A workgroup of linear_ring has the sums over its part of K.  True in the one of a tile's that
+// ends last, which then has all of them: the others' sums are in memory and it adds them.
+// Sums are written through to where every XCD sees them and read from there: fences, which
+// write back and empty an L2, took 50 us and more in all.
+__device__ __forceinline__ bool last_of_tile(const TileParams &p, i32x16 (&acc)[1][2], int id, int split, int wave, int lane) {
+    __shared__ int before;
+    const int all = p.m_tiles * p.n_tiles;
+    auto at = [&](int s) { return (uint64_t *)p.sums + ((int64_t)(s * all + id) * 2 + wave) * 1024 + lane; };
+    uint64_t *const mine = at(split);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            __hip_atomic_store(mine + (8 * j + r) * 64, (uint64_t)(uint32_t)acc[0][j][2 * r + 1] << 32 | (uint32_t)acc[0][j][2 * r],
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_s_waitcnt(0);  // they have arrived
+    asm volatile("" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) before = __hip_atomic_fetch_add(p.arrived + id, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (before != p.splits - 1) return false;
+    asm volatile("" ::: "memory");
+    for (int s = 0; s < p.splits; ++s) {
+        if (s == split) continue;
+        const uint64_t *const from = at(s);
+        uint64_t v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __hip_atomic_load(from + i * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            acc[0][i / 8][i % 8 * 2] += (int)(uint32_t)v[i];
+            acc[0][i / 8][i % 8 * 2 + 1] += (int)(uint32_t)(v[i] >> 32);
+        }
+    }
+    return true;
+}
+
 // The same for fewer tiles than keep every CU's matrix pipes fed: then a step is done long
 // before the next one's loads arrive, so that here the loads run four steps ahead, in
 // registers (which a wave has to spare), and pass into one of two LDS buffers a
@@ -393,9 +438,11 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64)) void linear_ring
     constexpr int kB = BM * 128;  // where a buffer's part of w begins
     __shared__ __attribute__((aligned(16))) int8_t lds[2][2 * kB];
     const int lane = (int)threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
-    const Tile t = place((int)blockIdx.x, p.m_tiles, p.n_tiles);
+    const int id = (int)blockIdx.x, split = MB == 1 ? (int)blockIdx.y : 0;
+    const Tile t = place(id, p.m_tiles, p.n_tiles);
     const int m0 = t.m * BM, n0 = t.n * BN;
-    const Loads loads(p, m0, n0, BN, wave, lane);
+    const int steps = p.l.Kp / 128, s0 = MB == 1 ? split * p.split_steps : 0;
+    const Loads loads(p, m0, n0, BN, wave, lane, s0, MB == 1 ? min(p.split_steps, steps - s0) : steps);
     const int wm = wave / kWavesN * 32 * MB, wn = wave % kWavesN * 64, r32 = lane % 32, half = lane / 32;
     const int swap = (r32 >> 1) & 7;
     i32x16 acc[MB][2] = {};
@@ -447,6 +494,8 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64)) void linear_ring
     if (s < loads.steps) turn(s, integral_constant<int, 0>{});
     if (s + 1 < loads.steps) turn(s + 1, integral_constant<int, 1>{});
     if (s + 2 < loads.steps) turn(s + 2, integral_constant<int, 2>{});
+    if constexpr (MB == 1)
+        if (p.splits > 1 && !last_of_tile(p, acc, id, split, wave, lane)) return;
     __syncthreads();
     static_assert(kTileBytes * kWaves <= 4 * kB, "");
     store_sums<T, SILU, MB>(p, acc, (int *)(lds[0] + wave * kTileBytes), m0 + wm, n0 + wn);
@@ -455,7 +504,7 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64)) void linear_ring
 // --- choice ----------------------------------------------------------------------
 
 // By the number of tiles that a kernel makes of the output, against the 256 CUs.  Where
-// the choice changes, measured at K 2048 and 8192, in us:
+// the choice changes, measured at K 2048 and 8192, in us (ring 64 with K whole; divided below):
 //   M x N         linear_stream   ring 64       ring 128      tile 256
 //   64 x 4096     10.0, 19.9      11.8, 24.2
 //   96 x 4096     12.4, 28.3      12.2, 24.6
@@ -478,7 +527,20 @@ Kind kind_of(int64_t M, int64_t N, int64_t K) {
     if (K % 16 != 0 && M <= 128) return kStream;
     if (tiles(M, N, 256) >= 192) return kTile256;
     if (tiles(M, N, 128) >= 160) return kRing128;
+    if (M > 32 && K > 6144) return kRing64;  // which divides K
     return tiles(M, N, 64) >= (M <= 32 ? 256 : 96) ? kRing64 : kStream;
+}
+// Workgroups of ring 64 that divide K: as many as leave one to a CU, with 16 steps for each, for
+// bringing the sums together takes as long as about 16.  Whole and divided, us:
+//   M x N         K 4096          K 8192        K 14336
+//   64 x 1024     11.7, 13.1      18.7, 16.4    29.6, 21.5
+//   96 x 4096     15.3, 14.1      24.0, 19.2    37.8, 27.4
+//   512 x 1024    17.4, 16.3      26.0, 21.3    40.2, 29.7
+//   256 x 4096    16.2, 17.7      24.7, 24.4    39.2, 36.5   (2 to a CU)
+// (64 x 1024 whole is linear_stream.)
+int splits_of(int64_t M, int64_t N, int64_t K) {
+    if (kind_of(M, N, K) != kRing64) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(256 / tiles(M, N, 64), (K + 127) / 128 / 16));
 }
 bool needs_copy(int64_t M, int64_t N, int64_t K) { return K % 16 != 0 && kind_of(M, N, K) != kStream; }
 
@@ -502,7 +564,7 @@ template <typename T> hipError_t launch_stream(const LinearArgs &a, const CodesL
         case 8: return launch_stream3<T, 1, 8>(p, st);
         case 16: return launch_stream3<T, 1, 16>(p, st);
     }
-    const hipError_t e = launch_quant_rows(a, l, nullptr, st);
+    const hipError_t e = launch_quant_rows(a, l, nullptr, nullptr, 0, st);
     if (e != hipSuccess) return e;
     // from here on x is not read: one type of the kernel serves all
     if (a.M <= 16) return launch_stream3<float, 1, 0>(p, st);
@@ -516,14 +578,19 @@ template <typename T, bool SILU> hipError_t launch2(const LinearArgs &a, const C
     const bool copy = needs_copy(a.M, a.N, a.K);
     // where only w's start is off 16 bytes there is no room for a copy
     if (kind == kStream || (!copy && (uintptr_t)a.w % 16 != 0)) return launch_stream<T>(a, l, st);
-    TileParams p{l, a.w, a.K, a.w_scale, a.bias, a.y, a.M, a.N, 0, 0};
+    TileParams p{l, a.w, a.K, a.w_scale, a.bias, a.y, a.M, a.N, 0, 0, 1, 0, nullptr, nullptr};
+    const int steps = l.Kp / 128, splits = splits_of(a.M, a.N, a.K), count = (int)tiles(a.M, a.N, 64);
+    p.split_steps = (steps + splits - 1) / splits;
+    p.splits = (steps + p.split_steps - 1) / p.split_steps;
     int8_t *const to = copy ? l.codes + (int64_t)l.rows * l.Kp : nullptr;
-    const hipError_t e = launch_quant_rows(a, l, to, st);
+    p.sums = (int *)(l.codes + (int64_t)l.rows * l.Kp + (copy ? (int64_t)a.N * l.Kp : 0));
+    p.arrived = p.sums + (int64_t)splits * count * 4096;
+    const hipError_t e = launch_quant_rows(a, l, to, p.splits > 1 ? p.arrived : nullptr, count, st);
     if (e != hipSuccess) return e;
     if (copy) p.w = to, p.w_stride = l.Kp;
     const int b = kind == kTile256 ? 256 : kind == kRing128 ? 128 : 64;
     p.m_tiles = (a.M + b - 1) / b, p.n_tiles = (a.N + b - 1) / b;
-    const unsigned grid = (unsigned)(p.m_tiles * p.n_tiles);
+    const dim3 grid(p.m_tiles * p.n_tiles, p.splits);
     if (kind == kTile256) linear_tile<T, SILU, 256, 256, 4><<<grid, 512, 0, st>>>(p);
     else if (kind == kRing128) linear_ring<T, SILU, 128, 128, 2><<<grid, 256, 0, st>>>(p);
     else linear_ring<T, SILU, 64, 64, 1><<<grid, 128, 0, st>>>(p);
@@ -537,7 +604,8 @@ template <typename T> hipError_t launch1(const LinearArgs &a, const CodesLayout 
 
 int64_t linear_workspace(int64_t M, int64_t N, int64_t K) {
     const CodesLayout l = codes_layout(nullptr, M, K);
-    return l.bytes + (needs_copy(M, N, K) ? N * l.Kp : 0);
+    const int64_t splits = splits_of(M, N, K);
+    return l.bytes + (needs_copy(M, N, K) ? N * l.Kp : 0) + (splits > 1 ? tiles(M, N, 64) * (splits * 16384 + 4) : 0);
 }
 
 hipError_t launch_int8_linear(const LinearArgs &a, int num_cu, hipStream_t st) {

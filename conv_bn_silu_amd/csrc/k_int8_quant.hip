@@ -44,23 +44,27 @@ __device__ __forceinline__ void store_chunk(int8_t *codes, int rows, int m, int 
 
 // Where the rows of w start at odd bytes, the tile kernels want them Kp apart: workgroups
 // beyond those of x copy them, 16 bytes a lane.
-struct RowCopy {
+struct Beside {
     const int8_t *w;
     int8_t *to;
     int N;
+    int *zeros;  // cleared by the first workgroup
+    int count;
 };
 
 // TEAM lanes per row: 64 or 256.
 template <typename T, int TEAM>
 __global__ __launch_bounds__(kThreads) void quant_rows(const T *__restrict__ x, int64_t x_stride, int M, int K, int Kp,
                                                        int rows, int8_t *__restrict__ codes,
-                                                       float *__restrict__ scales, const RowCopy copy) {
+                                                       float *__restrict__ scales, const Beside beside) {
     __shared__ uint32_t part[4];
+    if (blockIdx.x == 0)
+        for (int i = (int)threadIdx.x; i < beside.count; i += kThreads) beside.zeros[i] = 0;
     const int own = (M * TEAM + kThreads - 1) / kThreads;
     if ((int)blockIdx.x >= own) {
         const int64_t i = (int64_t)(blockIdx.x - own) * kThreads + threadIdx.x, n = i / (Kp / 16);
         const int k = (int)(i - n * (Kp / 16)) * 16;
-        if (n < copy.N) *(i32x4 *)(copy.to + n * Kp + k) = load_end(copy.w, n * K + k, (int64_t)copy.N * K);
+        if (n < beside.N) *(i32x4 *)(beside.to + n * Kp + k) = load_end(beside.w, n * K + k, (int64_t)beside.N * K);
         return;
     }
     const int m = (int)blockIdx.x * (kThreads / TEAM) + (int)threadIdx.x / TEAM;
@@ -94,16 +98,17 @@ __global__ __launch_bounds__(kThreads) void quant_rows(const T *__restrict__ x, 
     if (lane == 0) scales[m] = s;
 }
 
-template <typename T> hipError_t launch1(const LinearArgs &a, const CodesLayout &l, int8_t *to, hipStream_t st) {
+template <typename T>
+hipError_t launch1(const LinearArgs &a, const CodesLayout &l, int8_t *to, int *zeros, int count, hipStream_t st) {
     const T *x = (const T *)a.x;
-    const RowCopy copy{a.w, to, a.N};
+    const Beside beside{a.w, to, a.N, zeros, zeros ? count : 0};
     const int64_t more = to ? ((int64_t)a.N * (l.Kp / 16) + kThreads - 1) / kThreads : 0;
     if (a.K <= 2048)
         quant_rows<T, 64><<<(unsigned)((a.M + 3) / 4 + more), kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes,
-                                                                                 l.scales, copy);
+                                                                                 l.scales, beside);
     else
         quant_rows<T, 256><<<(unsigned)(a.M + more), kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes,
-                                                                        l.scales, copy);
+                                                                        l.scales, beside);
     return hipGetLastError();
 }
 
@@ -119,11 +124,11 @@ CodesLayout codes_layout(void *workspace, int64_t M, int64_t K) {
     return l;
 }
 
-hipError_t launch_quant_rows(const LinearArgs &a, const CodesLayout &l, int8_t *to, hipStream_t st) {
+hipError_t launch_quant_rows(const LinearArgs &a, const CodesLayout &l, int8_t *to, int *zeros, int count, hipStream_t st) {
     switch (a.dtype) {
-        case CBS_DTYPE_F32: return launch1<float>(a, l, to, st);
-        case CBS_DTYPE_BF16: return launch1<__bf16>(a, l, to, st);
-        default: return launch1<_Float16>(a, l, to, st);
+        case CBS_DTYPE_F32: return launch1<float>(a, l, to, zeros, count, st);
+        case CBS_DTYPE_BF16: return launch1<__bf16>(a, l, to, zeros, count, st);
+        default: return launch1<_Float16>(a, l, to, zeros, count, st);
     }
 }
 

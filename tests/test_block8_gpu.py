@@ -97,6 +97,35 @@ def test_linear_kernels(ops, shape):
         O.check(ops.int8_linear(x.cuda(), w.cuda(), ws.cuda(), b.cuda() if bias else None, act), ref, tol, f"{shape}")
 
 
+@pytest.mark.parametrize("shape", [(33, 64, 6272), (40, 70, 8192), (100, 1030, 8992), (130, 70, 6501),
+                                   (65, 16, 131072), (600, 200, 14336)], ids=lambda s: "x".join(map(str, s)))
+def test_linear_long_sums(ops, shape):
+    """Few outputs of long sums; calls one after the other share nothing."""
+    M, N, K = shape
+    for dtype, bias, act in ((BF16, False, None), (F32, True, "silu")):
+        say("[linear long sums]", shape, dtype)
+        x, w, ws, b = linear_inputs(M, N, K, dtype, M + N + K)
+        ref, tol = O.linear(x, w, ws, b if bias else None, act == "silu")
+        x, w, ws, b = x.cuda(), w.cuda(), ws.cuda(), b.cuda() if bias else None
+        y = [ops.int8_linear(x, w, ws, b, act) for _ in range(3)]
+        O.check(y[0], ref, tol, f"{shape}")
+        assert torch.equal(y[1], y[0]) and torch.equal(y[2], y[0])
+
+
+def test_linear_long_sums_graph(ops):
+    x, w, ws, b = (t.cuda() for t in linear_inputs(70, 200, 9216, BF16, 10))
+    want = ops.int8_linear(x, w, ws, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = ops.int8_linear(x, w, ws, b)
+    for i in range(4):
+        y.zero_()
+        graph.replay()
+        assert torch.equal(ops.int8_linear(x, w, ws, b), want), i
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+
+
 def test_linear_leading_axes_and_empty(ops):
     x, w, ws, b = linear_inputs(24, 48, 64, BF16, 5)
     ref, tol = O.linear(x, w, ws, b, True)
