@@ -27,6 +27,10 @@ template <typename C, int NB, int SPLIT> struct ManyShape {
     // waves fit a SIMD (2 prompts of 6000: 8 waves 469 us, 12 waves 407; with 8-bit
     // caches 543 and 593, for there it takes scratch memory or 168 registers of 196).
     static constexpr int kWaves = NB > 4 ? 4 : NB == 2 && !kI8 && SPLIT == 1 ? 12 : 8;
+    // A wave at its step goes before one that stages the next (2 prompts of 8192, 8 bits, 1317 ->
+    // 1302 us; 2 of 6000, 16 bits, 699 -> 689, dim 64 412 -> 401; 8 bits at dim 64 530 -> 546, dim
+    // 256 511 -> 514).
+    static constexpr bool kStepFirst = NB <= 4 && (NB > 2 || !kI8);
     static constexpr int kGroups = kWaves / SPLIT;  // waves with rows of their own
     static constexpr int kThreads = 64 * kWaves, kTile = 32 * kGroups, KS = KT * SPLIT;
     static constexpr int kPitchDims = NB <= 2 ? 64 : NB <= 4 ? 128 : 256;
@@ -304,6 +308,7 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
             // held: left alone the compiler reads each just before it is wanted, and waits.
             auto read_k = [&](int i) { return *(const X8 *)(lds + (k_at ^ (32 * (i / 2))) + 32 * (i % 2) * S::kPitch); };
             f32x16 s[2];
+            if (S::kStepFirst) __builtin_amdgcn_s_setprio(1);
             X8 ring[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) ring[i] = read_k(i);
@@ -388,6 +393,7 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+            if (S::kStepFirst) __builtin_amdgcn_s_setprio(0);
             l += sums[0] + sums[1];
             if (__builtin_expect(taken_out[buf][part] == j0, 0)) {
                 // what store() has taken out, to the rows that see it
