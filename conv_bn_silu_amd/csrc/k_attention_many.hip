@@ -10,8 +10,8 @@
 // leave its registers.
 //
 // Bound by the issue of vector and matrix instructions, which hardly overlap (57% and 34% of
-// a SIMD's cycles), and by power: 2 prompts of 8192, 32 heads over 8, dim 128, 8 bits: 1300
-// us, 0.85 PFLOP/s; a large library product reaches 1.13.
+// a SIMD's cycles), and by power: 2 prompts of 8192, 32 heads over 8, dim 128, 8 bits: 1310
+// us, 0.84 PFLOP/s; a large library product reaches 1.13.
 #include <hip/hip_runtime.h>
 
 #include "b8_attention.h"
