@@ -12,6 +12,8 @@
 // few rows: 4 us, the latency of one pass.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "b8_device.h"
 #include "b8_linear.h"
 
@@ -20,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunks = 4;  // of 8 values a lane keeps
+constexpr int kMostRows = 1 << 22;  // of x to a launch, and workgroups that copy w
 
 template <typename T> __device__ __forceinline__ f32x8 load_chunk(const T *row, int k, int K) {
     f32x8 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -45,10 +48,12 @@ __device__ __forceinline__ void store_chunk(int8_t *codes, int rows, int m, int 
 // Where the rows of w start at odd bytes, the tile kernels want them Kp apart: workgroups
 // beyond those of x copy them, 16 bytes a lane.
 struct Beside {
+    int own;  // workgroups that have rows of x
     const int8_t *w;
     int8_t *to;
     int N;
-    int *zeros;  // cleared by the first workgroup
+    int64_t first;  // 16-byte piece of the copy that they begin with
+    int *zeros;     // cleared by the first workgroup
     int count;
 };
 
@@ -60,9 +65,8 @@ __global__ __launch_bounds__(kThreads) void quant_rows(const T *__restrict__ x, 
     __shared__ uint32_t part[4];
     if (blockIdx.x == 0)
         for (int i = (int)threadIdx.x; i < beside.count; i += kThreads) beside.zeros[i] = 0;
-    const int own = (M * TEAM + kThreads - 1) / kThreads;
-    if ((int)blockIdx.x >= own) {
-        const int64_t i = (int64_t)(blockIdx.x - own) * kThreads + threadIdx.x, n = i / (Kp / 16);
+    if ((int)blockIdx.x >= beside.own) {
+        const int64_t i = beside.first + (int64_t)((int)blockIdx.x - beside.own) * kThreads + threadIdx.x, n = i / (Kp / 16);
         const int k = (int)(i - n * (Kp / 16)) * 16;
         if (n < beside.N) *(i32x4 *)(beside.to + n * Kp + k) = load_end(beside.w, n * K + k, (int64_t)beside.N * K);
         return;
@@ -100,16 +104,26 @@ __global__ __launch_bounds__(kThreads) void quant_rows(const T *__restrict__ x, 
 
 template <typename T>
 hipError_t launch1(const LinearArgs &a, const CodesLayout &l, int8_t *to, int *zeros, int count, hipStream_t st) {
-    const T *x = (const T *)a.x;
-    const Beside beside{a.w, to, a.N, zeros, zeros ? count : 0};
-    const int64_t more = to ? ((int64_t)a.N * (l.Kp / 16) + kThreads - 1) / kThreads : 0;
-    if (a.K <= 2048)
-        quant_rows<T, 64><<<(unsigned)((a.M + 3) / 4 + more), kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes,
-                                                                                 l.scales, beside);
-    else
-        quant_rows<T, 256><<<(unsigned)(a.M + more), kThreads, 0, st>>>(x, a.x_stride, a.M, a.K, l.Kp, l.rows, l.codes,
-                                                                        l.scales, beside);
-    return hipGetLastError();
+    const int64_t pieces = to ? (int64_t)a.N * (l.Kp / 16) : 0;
+    // one launch but for the largest sizes: a launch holds fewer than 2^32 threads
+    int64_t piece = 0;
+    for (int m0 = 0; m0 < a.M || piece < pieces; m0 += kMostRows) {
+        const T *x = (const T *)a.x + m0 * a.x_stride;
+        int8_t *const codes = l.codes + (int64_t)m0 * 64;
+        const int rows = std::max(0, std::min(kMostRows, a.M - m0)), own = a.K <= 2048 ? (rows + 3) / 4 : rows;
+        const int copies = (int)std::min<int64_t>(kMostRows, (pieces - piece + kThreads - 1) / kThreads);
+        const Beside beside{own, a.w, to, a.N, piece, zeros, zeros && m0 == 0 ? count : 0};
+        if (a.K <= 2048)
+            quant_rows<T, 64><<<(unsigned)(own + copies), kThreads, 0, st>>>(x, a.x_stride, rows, a.K, l.Kp, l.rows, codes,
+                                                                             l.scales + m0, beside);
+        else
+            quant_rows<T, 256><<<(unsigned)(own + copies), kThreads, 0, st>>>(x, a.x_stride, rows, a.K, l.Kp, l.rows, codes,
+                                                                              l.scales + m0, beside);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        piece += (int64_t)copies * kThreads;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
