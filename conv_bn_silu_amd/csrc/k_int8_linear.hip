@@ -43,6 +43,7 @@ struct StreamParams {
     int64_t x_stride;
     void *y;
     int M, N, K, dtype, act;
+    int m_tile;  // tile of rows of x that the launch begins with
 };
 
 template <typename T>
@@ -68,7 +69,7 @@ __global__ __launch_bounds__(kStreamThreads) void linear_stream(const StreamPara
     __shared__ uint32_t row_tops[kStreamWaves];
     const int lane = (int)threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
     const int row = lane % 16, group = lane / 16;
-    const int n0 = (int)blockIdx.x * 16 * NT, m0 = (int)blockIdx.y * 16 * MT;
+    const int n0 = (int)blockIdx.x * 16 * NT, m0 = ((int)blockIdx.y + p.m_tile) * 16 * MT;
     const int steps = p.l.Kp / 128, full = p.K / 128;  // the last step may be partial
     const int64_t size = (int64_t)p.N * p.K;
     const int8_t *wr[NT];
@@ -544,11 +545,17 @@ int splits_of(int64_t M, int64_t N, int64_t K) {
 }
 bool needs_copy(int64_t M, int64_t N, int64_t K) { return K % 16 != 0 && kind_of(M, N, K) != kStream; }
 
-template <typename T, int MT, int NT, int ROWS> hipError_t launch_stream4(const StreamParams &p, hipStream_t st) {
-    const dim3 grid((p.N + 16 * NT - 1) / (16 * NT), (p.M + 16 * MT - 1) / (16 * MT));
+template <typename T, int MT, int NT, int ROWS> hipError_t launch_stream4(StreamParams p, hipStream_t st) {
+    constexpr int kMost = 32768;  // tiles of rows to a launch: a grid's second dimension ends at 65535
+    const int m_tiles = (p.M + 16 * MT - 1) / (16 * MT);
     const size_t sums = (size_t)kStreamWaves * 16 * MT * 16 * NT * 4, codes = (size_t)ROWS * p.l.Kp;
-    linear_stream<T, MT, NT, ROWS><<<grid, kStreamThreads, sums > codes ? sums : codes, st>>>(p);
-    return hipGetLastError();
+    hipError_t e = hipSuccess;
+    for (; p.m_tile < m_tiles && e == hipSuccess; p.m_tile += kMost) {
+        const dim3 grid((p.N + 16 * NT - 1) / (16 * NT), std::min(kMost, m_tiles - p.m_tile));
+        linear_stream<T, MT, NT, ROWS><<<grid, kStreamThreads, sums > codes ? sums : codes, st>>>(p);
+        e = hipGetLastError();
+    }
+    return e;
 }
 template <typename T, int MT, int ROWS> hipError_t launch_stream3(const StreamParams &p, hipStream_t st) {
     // 32 rows of w to a workgroup where that leaves two for every CU, else 16
@@ -556,7 +563,7 @@ template <typename T, int MT, int ROWS> hipError_t launch_stream3(const StreamPa
     return two ? launch_stream4<T, MT, 2, ROWS>(p, st) : launch_stream4<T, MT, 1, ROWS>(p, st);
 }
 template <typename T> hipError_t launch_stream(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
-    const StreamParams p{l, a.w, a.w_scale, a.bias, a.x, a.x_stride, a.y, a.M, a.N, a.K, a.dtype, a.act};
+    const StreamParams p{l, a.w, a.w_scale, a.bias, a.x, a.x_stride, a.y, a.M, a.N, a.K, a.dtype, a.act, 0};
     switch (fused_rows(a.M, a.K)) {
         case 1: return launch_stream3<T, 1, 1>(p, st);
         case 2: return launch_stream3<T, 1, 2>(p, st);

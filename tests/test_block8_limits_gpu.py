@@ -48,3 +48,19 @@ def test_linear_most_rows(ops, M, N, K):
         assert torch.equal(y[m0:m0 + 2 ** 21], ops.int8_linear(x[m0:m0 + 2 ** 21], w, ws)), m0
     del x, y
     torch.cuda.empty_cache()
+
+
+def test_linear_most_rows_unaligned(ops):
+    """Weights that start off 16 bytes go through the streaming kernel, whose tiles of rows pass 65535 here."""
+    M, N, K = 64 * 65536 + 70, 5, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    say("[linear rows, unaligned]", M, N, K)
+    x = torch.empty(M, K, dtype=BF16, device="cuda").normal_(generator=g)
+    buf = torch.randint(-128, 128, (N * K + 1,), generator=g, dtype=torch.int32, device="cuda").to(I8)
+    w = buf[1:].view(N, K)
+    ws = torch.rand(N, generator=g, device="cuda") * 0.02 + 0.001
+    y = ops.int8_linear(x, w, ws)
+    at = rows_at(M, [64 * 32768, 64 * 65535, 64 * 65536])
+    ref, tol = O.linear(x[at.cuda()].cpu(), w.cpu(), ws.cpu(), None, False)
+    O.check(y[at.cuda()], ref, tol, f"{M} {N} {K}")
+    assert torch.equal(y, ops.int8_linear(x, w.clone(), ws))
