@@ -10,6 +10,7 @@
 // x 128, bf16: written and read back in 86 us, 4.7 TB/s.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "b8_device.h"
@@ -23,7 +24,7 @@ constexpr int kThreads = 256;
 struct CacheParams {
     CacheIo io;
     FastDiv heads, page;
-    uint32_t rows;   // tokens * heads
+    uint32_t rows;   // tokens * heads of the launch
     uint32_t slots;  // pages * page size
 };
 
@@ -102,17 +103,28 @@ __global__ __launch_bounds__(kThreads) void cache_read(const CacheParams p) {
     Value<T>::store8((T *)(second ? p.io.v_out : p.io.k_out) + (int64_t)row * dim + d, x);
 }
 
-CacheParams params(const CacheIo &a) {
-    return CacheParams{a, make_fastdiv((uint32_t)a.cache.heads), make_fastdiv((uint32_t)a.cache.page_size),
-                       (uint32_t)(a.tokens * a.cache.heads), (uint32_t)(a.cache.pages * a.cache.page_size)};
-}
-
 template <typename T, typename C, int TEAM> hipError_t launch3(const CacheIo &a, bool write, hipStream_t st) {
-    const CacheParams p = params(a);
-    const unsigned grid = (p.rows + kThreads / TEAM - 1) / (kThreads / TEAM);
-    if (write) cache_write<T, C, TEAM><<<grid, kThreads, 0, st>>>(p);
-    else cache_read<T, C, TEAM><<<dim3(grid, 2), kThreads, 0, st>>>(p);
-    return hipGetLastError();
+    // one launch but for the largest calls: a launch holds fewer than 2^32 threads
+    const int64_t heads = a.cache.heads, most = std::max<int64_t>(1, (1 << 26) / heads);
+    hipError_t e = hipSuccess;
+    for (int64_t t = 0; t < a.tokens && e == hipSuccess; t += most) {
+        CacheParams p{a, make_fastdiv((uint32_t)heads), make_fastdiv((uint32_t)a.cache.page_size), 0,
+                      (uint32_t)(a.cache.pages * a.cache.page_size)};
+        p.rows = (uint32_t)(std::min(most, a.tokens - t) * heads);
+        p.io.slots += t;
+        const unsigned grid = (p.rows + kThreads / TEAM - 1) / (kThreads / TEAM);
+        if (write) {
+            p.io.k = (const T *)a.k + t * a.k_token;
+            p.io.v = (const T *)a.v + t * a.v_token;
+            cache_write<T, C, TEAM><<<grid, kThreads, 0, st>>>(p);
+        } else {
+            p.io.k_out = (T *)a.k_out + t * heads * a.cache.dim;
+            p.io.v_out = (T *)a.v_out + t * heads * a.cache.dim;
+            cache_read<T, C, TEAM><<<dim3(grid, 2), kThreads, 0, st>>>(p);
+        }
+        e = hipGetLastError();
+    }
+    return e;
 }
 template <typename T, typename C> hipError_t launch2(const CacheIo &a, bool write, hipStream_t st) {
     return a.cache.dim <= 128 ? launch3<T, C, 16>(a, write, st) : launch3<T, C, 32>(a, write, st);

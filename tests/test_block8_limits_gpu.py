@@ -64,3 +64,27 @@ def test_linear_most_rows_unaligned(ops):
     ref, tol = O.linear(x[at.cuda()].cpu(), w.cpu(), ws.cpu(), None, False)
     O.check(y[at.cuda()], ref, tol, f"{M} {N} {K}")
     assert torch.equal(y, ops.int8_linear(x, w.clone(), ws))
+
+
+@pytest.mark.parametrize("tokens,heads,dim", [(2 ** 28 + 5, 1, 8), (2 ** 26 + 3, 2, 136)], ids=["narrow", "wide"])
+def test_cache_most_rows(ops, tokens, heads, dim):
+    """Calls of more rows than a launch has threads for (16 lanes a row up to dim 128, 32 beyond)."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    say("[cache rows]", tokens, heads, dim)
+    pages, page = 64, 16
+    cache = ops.PagedCache.empty(pages, heads, page, dim)
+    k = torch.empty(tokens, heads, dim, dtype=BF16, device="cuda").normal_(generator=g)
+    # tokens from all over the call have slots, the others none
+    at = torch.cat([torch.arange(400), tokens // 2 + torch.arange(200), tokens - 1 - torch.arange(400)]).cuda()
+    slots = torch.full((tokens,), -1, dtype=torch.int32, device="cuda")
+    slots[at] = torch.randperm(pages * page, generator=g, device="cuda")[:at.numel()].to(torch.int32)
+    ops.cache_write(cache, k, k, slots)
+    codes, s = O.quantize(k[at].cpu())
+    want = (codes.float() * s[..., None]).to(BF16)
+    del k
+    got = ops.cache_read(cache, slots, BF16)
+    for y in got:
+        assert torch.equal(y[at].cpu(), want)
+        assert int(torch.count_nonzero(y)) == int(torch.count_nonzero(want))  # and zeros elsewhere
+    del got, y
+    torch.cuda.empty_cache()
