@@ -21,9 +21,15 @@
 // Queries in bf16 become fp16 after a power of two per row, which brings the
 // row's largest to [2^14, 2^15): values down to 2^-28 of the largest stay exact, smaller
 // ones are off by 2^-39 of it, below what the fp32 sum of the products loses.
-// A value's scale goes into its probability, divided by a running power of two
-// above the largest scale seen, so that the product fits fp16 whatever
-// the scales; the outputs are kept in units of that power.
+// A value's scale goes into its probability, and the product, like the queries, into
+// fp16 (10 bits after the point: half a step of 2^-11 of each, and what lies below 2^-24 of
+// half of the row's largest product is off by up to half of that).  So that it fits whatever the scales,
+// each row keeps two exponents: `m` of its largest probability, in whose unit the sum is kept, and `mo`, 2^6
+// below its largest product of probability and scale, in whose unit the outputs are.  Both follow
+// only what the row sees: a key behind the mask may have any scale, and so may one of negligible weight.
+// Where the scales of a tile lie within 2^7 of each other (nearly always), one
+// power of two above stands for all of them in mo, and goes into the exponent of the
+// probabilities; else the largest product is looked for (see `ValueUnit`).
 #pragma once
 
 #include "b8_launch.h"
@@ -61,6 +67,7 @@ int many_tile(int64_t dim, bool int8, bool split);  // rows of its tile
 #ifdef __HIPCC__
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;  // of the running maximum, as an exponent of two
+constexpr float kLift = 6.f;   // of the products with an 8-bit value's scale, which 2^(8 + 6) keeps within fp16
 
 struct Sequence {
     int b, first, n, len;  // its rows of q and the tokens it has in the cache
@@ -171,9 +178,47 @@ template <typename X> struct Parts {
 // A key's scale: under an infinite one its elements are infinities of both signs, or NaN
 // where the code is 0, and so its score is NaN, not the infinity that scaling the sum gives.
 __device__ __forceinline__ float finite_or_nan(float s) { return __builtin_isfinite(s) ? s : NAN; }
-// A power of two above the scale with these bits (a finite one), at most 2^127.
-__device__ __forceinline__ float power_above(uint32_t bits) {
-    return __uint_as_float(min((bits & 0x7F800000u) + 0x00800000u, 0x7F000000u));
+
+// How the value scales of a tile of keys enter, one key a lane; the same for all lanes.
+constexpr float kUneven = 1024.f;  // in place of the exponent
+struct ValueUnit {
+    int exp = 0;  // biased exponent of a power of two above the scales of the last even tile
+    // `bits` of the magnitude of the lane's scale; `counts` where its key is in the cache and the scale finite.
+    // Returns the exponent of the power by which the tile's scales are to be divided, or kUneven where they stay
+    // as they are.
+    __device__ __forceinline__ float of_tile(uint32_t bits, bool counts) {
+        const int e = (int)(bits >> 23);
+        if (__any(counts && (e >= exp || e < exp - 7))) {
+            int most = counts ? e : 0, least = counts ? e : 255;
+#pragma unroll
+            for (int x = 1; x < 64; x *= 2) {
+                most = max(most, __shfl_xor(most, x, 64));
+                least = min(least, __shfl_xor(least, x, 64));
+            }
+            most = __builtin_amdgcn_readfirstlane(most), least = __builtin_amdgcn_readfirstlane(least);
+            if (most - least > 6) return kUneven;
+            exp = most + 1;
+        }
+        return (float)(exp - 127);
+    }
+};
+__device__ __forceinline__ float in_unit(float scale, float unit) {
+    return unit == kUneven ? scale : __builtin_amdgcn_ldexpf(scale, -(int)unit);
+}
+// A row's exponents, before it has seen anything: below all others, and yet a number.
+constexpr float kNoExponent = -3.4028235e38f;
+// mo after a tile whose largest product has the exponent u.
+__device__ __forceinline__ float product_exponent(float mo, float u) { return u > mo + (kSlack + kLift) ? u - kLift : mo; }
+// The exponent that a tile's probabilities are taken relative to.  Where it is kFar above m the
+// products are nothing in fp16 (below 2^-46), while the sum still gets what the row sees.
+constexpr float kFar = 60.f;
+__device__ __forceinline__ float tile_exponent(float m, float mo, float unit) {
+    return unit == kUneven ? m : fminf(mo - unit, m + kFar);
+}
+// An uneven tile's scale for a row: the product with the probability 2^(x - m) is in the row's unit.
+__device__ __forceinline__ float uneven_scale(float scale, float m, float mo) {
+    const float v = scale * fminf(__builtin_amdgcn_exp2f(m - mo), 0x1p126f);
+    return __builtin_isinf(v) && __builtin_isfinite(scale) ? copysignf(0x1p126f, scale) : v;
 }
 // An output and its sum: zeros where no key was seen.
 __device__ __forceinline__ float divide(float o, float l) { return l > 0.f || l != l ? o / l : 0.f; }

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                 raw[s] = u32x4{0u, 0u, 0u, 0u};
                 if (dims(s) < dim) raw[s] = ((const Any16 *)(src + dims(s)))->v ^ flip;
             }
-            qf[i] = c0;
+            qf[i] = fmaxf(c0, 0x1p-149f);  // above zero, so that -inf stays what it is
             if constexpr (std::is_same_v<X, T>) {
 #pragma unroll
                 for (int s = 0; s < S::kSteps; ++s) q[i][s] = __builtin_bit_cast(X8, raw[s]);
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                 top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
                 // exponent 14 for the largest; rows of infinities and NaN stay as they are
                 const int e = top >= 0x7F80u ? 0 : min(126, 141 - (int)(top >> 7));
-                qf[i] = __builtin_ldexpf(c0, -e);
+                qf[i] = fmaxf(__builtin_ldexpf(c0, -e), 0x1p-149f);
                 const float up = __builtin_ldexpf(1.f, e);
 #pragma unroll
                 for (int s = 0; s < S::kSteps; ++s) {
@@ -133,9 +133,11 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
         }
 
         f32x4 o[QT][S::kDims / 16] = {};
-        float m[QT], l[QT], vref = 0x1p-126f;
+        // 8-bit caches: m and mo are exponents; else m is a score, and the outputs are in its unit
+        float m[QT], l[QT], mo[QT];
 #pragma unroll
-        for (int i = 0; i < QT; ++i) m[i] = -INFINITY, l[i] = 0.f;
+        for (int i = 0; i < QT; ++i) m[i] = S::kI8 ? kNoExponent : -INFINITY, mo[i] = kNoExponent, l[i] = 0.f;
+        ValueUnit units;
 
         // the tile in registers, and what belongs to it; lane i has key j0 + i
         u32x4 kreg[KB][S::kRow / 64], vreg[S::kLoads];
@@ -201,20 +203,12 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                     for (int i = 0; i < QT; ++i) s[i][kb] = mma16(kf, q[i][st], s[i][kb]);
                 }
             // this tile's scales and values to LDS, the next tile's on their way
-            float fade_v = 1.f;
+            float unit = 0.f;
             if constexpr (S::kI8) {
                 const uint32_t bits = magnitude(vs);
-                const bool counts = ((valid >> (lane % KT)) & 1) && bits < 0x7F800000u;
-                if (__any(counts && vs > vref)) {
-                    uint32_t top = counts ? bits : 0u;
-#pragma unroll
-                    for (int x = 1; x < 64; x *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, x, 64));
-                    const float now = power_above(top);
-                    fade_v = vref / now;
-                    vref = now;
-                }
+                unit = units.of_tile(bits, ((valid >> (lane % KT)) & 1) && bits < 0x7F800000u);
                 kscale[lane % KT] = finite_or_nan(ks);
-                vscale[lane % KT] = vs * (1.f / vref);
+                vscale[lane % KT] = in_unit(vs, unit);
             }
             // LDS addresses are made anew for each tile: kept, they cost a register for each access
             int my = lane, my_col = col;
@@ -272,17 +266,54 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                     top = fmaxf(top, fmaxf(fmaxf(s[i][kb][0], s[i][kb][1]), fmaxf(s[i][kb][2], s[i][kb][3])));
                 top = fmaxf(top, __shfl_xor(top, 16, 64));
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const bool move = top > m[i] && !((top - m[i]) * qf[i] <= kSlack);
-                if (__any(move) || fade_v != 1.f) {
-                    const float now = move ? top : m[i];
-                    const float fade = move ? (m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[i] - now) * qf[i])) : 1.f;
-                    m[i] = now;
-                    l[i] *= fade;
-                    const float both = fade * fade_v;
+                float base, to_sum = 1.f;
+                if constexpr (S::kI8) {
+                    const float x = top * qf[i];
+                    float u = x + unit;
+                    if (unit == kUneven) {
+                        u = -INFINITY;
 #pragma unroll
-                    for (int d = 0; d < S::kDims / 16; ++d) o[i][d] *= both;
+                        for (int kb = 0; kb < KB; ++kb) {
+                            __builtin_amdgcn_sched_barrier(0);  // rare: no registers to work on several at once
+                            const f32x4 v = *(const f32x4 *)(vscale + 16 * kb + 4 * grp);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                u = fmaxf(u, __builtin_fmaf(s[i][kb][e], qf[i], __builtin_amdgcn_logf(fabsf(v[e]))));
+                        }
+                        u = fmaxf(u, __shfl_xor(u, 16, 64));
+                        u = fmaxf(u, __shfl_xor(u, 32, 64));
+                    }
+                    const float now = x > m[i] + kSlack ? x : m[i], now_o = product_exponent(mo[i], u);
+                    if (__any(now != m[i] || now_o != mo[i])) {
+                        l[i] *= __builtin_amdgcn_exp2f(m[i] - now);
+                        const float fade = __builtin_amdgcn_exp2f(mo[i] - now_o);
+                        m[i] = now, mo[i] = now_o;
+#pragma unroll
+                        for (int d = 0; d < S::kDims / 16; ++d) o[i][d] *= fade;
+                    }
+                    if (unit == kUneven) {
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            vsc[kb] = *(const f32x4 *)(vscale + 16 * kb + 4 * grp);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) vsc[kb][e] = uneven_scale(vsc[kb][e], m[i], mo[i]);
+                        }
+                    }
+                    base = tile_exponent(m[i], mo[i], unit);
+                    to_sum = __builtin_amdgcn_exp2f(base - m[i]);
+                } else {
+                    const bool move = top > m[i] && !((top - m[i]) * qf[i] <= kSlack);
+                    if (__any(move)) {
+                        const float now = move ? top : m[i];
+                        const float fade = move ? (m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[i] - now) * qf[i])) : 1.f;
+                        m[i] = now;
+                        l[i] *= fade;
+#pragma unroll
+                        for (int d = 0; d < S::kDims / 16; ++d) o[i][d] *= fade;
+                    }
+                    base = m[i] == -INFINITY ? 0.f : m[i] * qf[i];
                 }
-                const float base = m[i] == -INFINITY ? 0.f : m[i] * qf[i];
                 float sum = 0.f;
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
@@ -297,7 +328,7 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                         }
                         pr[i][kb / 2][kb % 2 * 4 + e] = (X)w;
                     }
-                l[i] += sum;
+                l[i] += sum * to_sum;
             }
 
             // values: keys 32 t + 4 grp + 0..3 and 16 above those, of dim 16 db + col
@@ -362,12 +393,14 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
             sum += __shfl_xor(sum, 32, 64);
             const int row = wave * 16 * QT + 16 * i + col;
             if (grp == 0) {
-                pm[2 * row] = m[i] == -INFINITY ? -INFINITY : m[i] * qf[i];
+                if constexpr (S::kI8) pm[2 * row] = m[i] == kNoExponent ? -INFINITY : m[i];
+                else pm[2 * row] = m[i] == -INFINITY ? -INFINITY : m[i] * qf[i];
                 pm[2 * row + 1] = sum;
             }
+            const float unit = S::kI8 ? __builtin_amdgcn_exp2f(mo[i] - m[i]) : 1.f;
 #pragma unroll
             for (int db = 0; db < S::kDims / 16; ++db)
-                *(f32x4 *)(po + row * S::kOutPitch + 16 * db + 4 * grp) = S::kI8 ? o[i][db] * vref : o[i][db];
+                *(f32x4 *)(po + row * S::kOutPitch + 16 * db + 4 * grp) = o[i][db] * unit;
         }
         __syncthreads();
         for (int e = (int)threadIdx.x; e < (r1 - r0) * S::kDims; e += kThreads) {

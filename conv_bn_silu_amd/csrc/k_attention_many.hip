@@ -117,7 +117,7 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
     __shared__ __attribute__((aligned(16))) unsigned char lds[S::kBytes];
     __shared__ __attribute__((aligned(16))) float kscale[2][KS], vscale[2][KS];
     __shared__ uint64_t valid_bits[2][SPLIT];
-    __shared__ float vrefs[2][SPLIT];
+    __shared__ float units[2][SPLIT];  // ValueUnit::of_tile
     __shared__ int taken_out[2][SPLIT];  // the last step in whose values store() found something to take out
     const AttentionArgs &a = p.a;
     const int tid = (int)threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -191,7 +191,8 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
     u32x4 kreg[S::kLoads], vreg[S::kLoads];
     bool vok[S::kLoads];
     int next_page[S::kLoads], key_page = -1;
-    float ks = 0.f, vs = 0.f, vref = 0x1p-126f;
+    float ks = 0.f, vs = 0.f;
+    ValueUnit value_unit;
     uint64_t key_bits = 0;
     auto page_of = [&](int j) { return j < hi ? table[p.page.div((uint32_t)j)] : -1; };
     auto row_of = [&](int j, int page, bool &ok) {
@@ -264,15 +265,10 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
                 const uint64_t taken = __ballot(there && !counts);
                 if (taken && lane == 0) taken_out[buf][part] = j0;
                 if (!counts) vs = 0.f;
-                if (__any(vs > vref)) {
-                    uint32_t top = counts ? bits : 0u;
-#pragma unroll
-                    for (int x = 1; x < 64; x *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, x, 64));
-                    vref = power_above(top);
-                }
+                const float unit = value_unit.of_tile(bits, counts);
                 kscale[buf][KT * part + lane] = finite_or_nan(ks);
-                vscale[buf][KT * part + lane] = vs * (1.f / vref);
-                if (lane == 0) vrefs[buf][part] = vref;
+                vscale[buf][KT * part + lane] = in_unit(vs, unit);
+                if (lane == 0) units[buf][part] = unit;
             }
             if (lane == 0) valid_bits[buf][part] = key_bits;
         }
@@ -283,7 +279,8 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
     const int v_lane = v_row * S::kPitch + (((2 * (lane / 16 % 2) + lane % 4 / 2) ^ S::swap_v(v_row)) * 16) + lane % 2 * 8;
 
     f32x16 o[NB] = {};
-    float m = -INFINITY, l = 0.f, o_ref = 0x1p-126f;
+    // 8-bit caches: m and mo are exponents; else m is a score, and the outputs are in its unit
+    float m = S::kI8 ? kNoExponent : -INFINITY, l = 0.f, mo = kNoExponent;
 
     if (tid < 2 * SPLIT) taken_out[tid / SPLIT][tid % SPLIT] = -1;
     __syncthreads();
@@ -349,22 +346,44 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) tops[kb] = fmaxf(fmaxf(tops[kb], s[kb][i]), s[kb][i + 1]);
             const float top = max_halves(fmaxf(fmaxf(fmaxf(tops[0], s[0][15]), tops[1]), s[1][15]));
-            const bool move = top > m && !((top - m) * qf <= kSlack);
-            float ref = o_ref;
-            if constexpr (S::kI8) ref = vrefs[buf][part];
-            if (__any(move || ref != o_ref)) {
-                const float now = move ? top : m;
-                const float fade = move ? (m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - now) * qf)) : 1.f;
-                m = now;
-                l *= fade;
-                const float both = fade * (o_ref / ref);
-                o_ref = ref;
-#pragma unroll
-                for (int db = 0; db < NB; ++db) o[db] *= both;
-            }
+            float base, to_sum = 1.f;
             if constexpr (S::kI8) {
+                const float unit = units[buf][part], x = top * qf;
 #pragma unroll
                 for (int g = 0; g < 8; ++g) per_key[g] = *(const f32x4 *)(&vscale[buf][KT * part + 8 * g + 4 * half]);
+                float u = x + unit;
+                if (__builtin_expect(__any(unit == kUneven), 0)) {
+                    u = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        u = fmaxf(u, __builtin_fmaf(s[i / 16][i % 16], qf, __builtin_amdgcn_logf(fabsf(per_key[i / 4][i % 4]))));
+                    u = max_halves(u);
+                }
+                const float now = x > m + kSlack ? x : m, now_o = product_exponent(mo, u);
+                if (__any(now != m || now_o != mo)) {
+                    l *= __builtin_amdgcn_exp2f(m - now);
+                    const float fade = __builtin_amdgcn_exp2f(mo - now_o);
+                    m = now, mo = now_o;
+#pragma unroll
+                    for (int db = 0; db < NB; ++db) o[db] *= fade;
+                }
+                if (__builtin_expect(__any(unit == kUneven), 0)) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) per_key[i / 4][i % 4] = uneven_scale(per_key[i / 4][i % 4], m, mo);
+                }
+                base = tile_exponent(m, mo, unit);
+                to_sum = __builtin_amdgcn_exp2f(base - m);
+            } else {
+                const bool move = top > m && !((top - m) * qf <= kSlack);
+                if (__any(move)) {
+                    const float now = move ? top : m;
+                    const float fade = move ? (m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - now) * qf)) : 1.f;
+                    m = now;
+                    l *= fade;
+#pragma unroll
+                    for (int db = 0; db < NB; ++db) o[db] *= fade;
+                }
+                base = m == -INFINITY ? 0.f : m * qf;
             }
             // values: keys 16 t + 4 half + 0..3 and 8 above those, of dim 32 db + col
             auto read_v = [&](int i) {
@@ -376,7 +395,6 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
             for (int i = 0; i < kAhead; ++i) ring[i] = read_v(i);
             __builtin_amdgcn_sched_barrier(0);
             // a key that is not seen: 2^-inf = 0
-            const float base = m == -INFINITY ? 0.f : m * qf;
             float sums[2] = {0.f, 0.f};
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -398,7 +416,7 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (S::kStepFirst) __builtin_amdgcn_s_setprio(0);
-            l += sums[0] + sums[1];
+            l += (sums[0] + sums[1]) * to_sum;
             if (__builtin_expect(taken_out[buf][part] == j0, 0)) {
                 // what store() has taken out, to the rows that see it
 #pragma unroll 1
@@ -429,7 +447,9 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
     }
 
     // the lane has one row, of every 32 dims 16
-    float ref = S::kI8 ? o_ref : 1.f, top = m == -INFINITY ? -INFINITY : m * qf;  // units of the outputs and exponents
+    float ref = 1.f, top;  // the outputs' unit in that of the sum, whose exponent is top
+    if constexpr (S::kI8) ref = __builtin_amdgcn_exp2f(mo - m), top = m == kNoExponent ? -INFINITY : m;
+    else top = m == -INFINITY ? -INFINITY : m * qf;
     if constexpr (SPLIT == 2) {
         // the second half of the waves hand theirs over, lane by lane
         __syncthreads();
@@ -501,7 +521,7 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
             typedef T x4 __attribute__((ext_vector_type(4)));
             x4 v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (T)divide(o[db][4 * g + e] * ref, sum);
+            for (int e = 0; e < 4; ++e) v[e] = (T)(divide(o[db][4 * g + e], sum) * ref);
             *(x4 *)(stage + col * S::kOutPitch + 2 * (32 * db + 8 * g + 4 * half)) = v;
         }
     __builtin_amdgcn_wave_barrier();
