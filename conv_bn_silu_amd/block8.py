@@ -98,7 +98,8 @@ def cache_write(cache: PagedCache, k, v, slots, library: Library | None = None):
     head) where it is int8.
 
     k, v: [tokens, heads, dim] float32, bfloat16 or float16, dim contiguous;
-    slots: int32 [tokens]; a token whose slot is outside the cache is skipped.
+    slots: int32 [tokens]; a token whose slot is outside the cache is skipped, and
+    no two may name one slot (what that holds afterwards is undefined).
     """
     _checked(_block8.cache_write(_handle(library), cache._record, k, v, slots), library, "cbs_cache_write")
 

@@ -68,15 +68,18 @@ typedef struct cbs_paged_cache {
  * its type (round to nearest even).
  *   k, v: [tokens][heads][dim] of dtype (F32, BF16 or F16), token and head
  *      strides in elements, dim contiguous; slots: int32 [tokens].
- * A token whose slot lies outside [0, pages * page_size) is skipped.  Where two
- * tokens name one slot, either is written.  k and v must not overlap the cache. */
+ * A token whose slot lies outside [0, pages * page_size) is skipped.  No two tokens
+ * of a call may name one slot: what such a slot holds afterwards is undefined (codes
+ * of one token may stand under the scale of the other); the other slots are written as
+ * ever.  k and v must not overlap the cache. tokens * heads is below 2^31, else
+ * CBS_ERR_UNSUPPORTED. */
 int cbs_cache_write(conv_bn_silu_t handle, const cbs_paged_cache *cache, const void *k, int64_t k_token_stride,
                     int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
                     const int32_t *slots, int64_t tokens, int dtype, void *stream);
 
 /* Read tokens back: k_out, v_out contiguous [tokens][heads][dim] of dtype;
  * code * scale (or the stored value) rounded once.  A slot outside the cache
- * reads as zeros. */
+ * reads as zeros; tokens may name one slot here.  tokens * heads is below 2^31. */
 int cbs_cache_read(conv_bn_silu_t handle, const cbs_paged_cache *cache, const int32_t *slots, int64_t tokens,
                    void *k_out, void *v_out, int dtype, void *stream);
 
