@@ -76,13 +76,17 @@ class PagedCache:
 
     k, v: contiguous [pages, heads, page_size, dim], int8 (with k_scale, v_scale:
     float32 [pages, heads, page_size]) or float32, bfloat16, float16 (without).
-    A token's slot is page * page_size + offset.
+    A token's slot is page * page_size + offset.  The tensors' contents may be changed
+    at will; other tensors take a PagedCache of their own.
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self._record = _block8.cache(k, v, k_scale, v_scale)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = k, v, k_scale, v_scale
         self.pages, self.heads, self.page_size, self.dim = k.shape
+
+    # what the kernels are given is the record's, so these cannot be set
+    k, v, k_scale, v_scale = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
 
     @classmethod
     def empty(cls, pages, heads, page_size, dim, dtype=torch.int8, device="cuda"):

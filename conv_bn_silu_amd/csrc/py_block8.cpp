@@ -149,15 +149,24 @@ PyObject *int8_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// A cache's record, in a capsule; the PagedCache that owns it keeps its tensors.
+// A cache's record, in a capsule: the tensors, and their addresses as the C ABI takes them.
 struct Record {
     cbs_paged_cache c;
-    at::Tensor k;
+    at::Tensor k, v, k_scale, v_scale;
+    int64_t elements;
+    // The tensors' memory may be exchanged under the record (set_, resize_, an assignment to .data).
+    bool holds() const {
+        if (k.data_ptr() != c.k || v.data_ptr() != c.v || k.numel() != elements || v.numel() != elements) return false;
+        if (!k_scale.defined()) return true;
+        return k_scale.data_ptr() == c.k_scale && v_scale.data_ptr() == c.v_scale && k_scale.numel() * c.dim == elements &&
+               v_scale.numel() * c.dim == elements;
+    }
 };
 constexpr const char *kCapsule = "conv_bn_silu_amd.cache";
 const Record &record(PyObject *o) {
     const Record *r = (const Record *)PyCapsule_GetPointer(o, kCapsule);
     if (!r) throw Refused();
+    if (!r->holds()) refuse(PyExc_ValueError, "the cache's tensors have been given other memory: make a PagedCache of them");
     return *r;
 }
 // (k, v, k_scale, v_scale) -> capsule
@@ -168,22 +177,22 @@ PyObject *cache(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (k.dim() != 4) refuse(PyExc_ValueError, "k must be [pages, heads, page_size, dim]");
         contiguous(k, k.sizes(), "k");
         contiguous(v, k.sizes(), "v");
-        void *scales[2] = {nullptr, nullptr};
+        at::Tensor scales[2];
         if (k.scalar_type() == at::kChar) {
             for (int i = 0; i < 2; ++i) {
                 const char *what = i ? "v_scale" : "k_scale";
                 const at::Tensor &s = tensor(a[2 + i], what, {at::kFloat}, &k);
                 contiguous(s, k.sizes().slice(0, 3), what);
-                scales[i] = s.data_ptr();
+                scales[i] = s;
             }
         } else if (a[2] != Py_None || a[3] != Py_None) {
             refuse(PyExc_ValueError, "only an int8 cache has scales");
         }
         for (int i = 1; i < 4; ++i)
             if (k.size(i) > INT32_MAX) refuse(PyExc_ValueError, "k must be [pages, heads, page_size, dim]");
-        Record *r = new Record{{k.data_ptr(), v.data_ptr(), (float *)scales[0], (float *)scales[1], k.size(0),
+        Record *r = new Record{{k.data_ptr(), v.data_ptr(), (float *)data(scales[0]), (float *)data(scales[1]), k.size(0),
                                 (int32_t)k.size(1), (int32_t)k.size(2), (int32_t)k.size(3), code_of(k.scalar_type())},
-                               k};
+                               k, v, scales[0], scales[1], k.numel()};
         PyObject *c = PyCapsule_New(r, kCapsule, [](PyObject *o) { delete (Record *)PyCapsule_GetPointer(o, kCapsule); });
         if (!c) delete r;
         return c;

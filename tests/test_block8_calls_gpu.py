@@ -35,3 +35,42 @@ def test_shared_slots_harm_no_others(ops, held):
     unnamed = torch.ones(800, dtype=torch.bool)
     unnamed[slots.long()] = False
     assert bool((ops.cache_read(cache, unnamed.nonzero()[:, 0].to(torch.int32).cuda())[0] == 0).all())
+
+
+def test_a_cache_keeps_its_tensors(ops):
+    """The memory that the kernels are given is not freed while the cache lives, and a cache whose tensors
+    have been given other memory is refused."""
+    dev = dict(device="cuda")
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    cache = ops.PagedCache.empty(64, 2, 16, 64)
+    held = torch.cuda.memory_allocated() - before
+    record = cache._record
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, torch.zeros_like(getattr(cache, name)))
+    del cache
+    assert torch.cuda.memory_allocated() - before == held > 64 * 2 * 16 * 64 * 2
+    del record
+    assert torch.cuda.memory_allocated() == before
+
+    slots = torch.zeros(1, dtype=torch.int32, **dev)
+    x = torch.zeros(1, 2, 64, dtype=BF16, **dev)
+    i32 = dict(dtype=torch.int32, **dev)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        for how in ("data", "set_", "resize_"):
+            cache = ops.PagedCache.empty(64, 2, 16, 64)
+            t = getattr(cache, name)
+            old = t.detach()
+            if how == "data":
+                t.data = torch.zeros_like(t)
+            elif how == "set_":
+                t.set_(torch.zeros_like(t))
+            else:
+                t.resize_(0)
+            for call in (lambda: ops.cache_write(cache, x, x, slots), lambda: ops.cache_read(cache, slots),
+                         lambda: ops.paged_attention(x, cache, torch.zeros(1, 1, **i32), torch.tensor([0, 1], **i32),
+                                                     torch.ones(1, **i32))):
+                with pytest.raises(ValueError, match="other memory"):
+                    call()
+            del old
