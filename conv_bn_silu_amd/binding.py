@@ -207,6 +207,8 @@ def _geometry(x, w, scale, bias, stride, pad):
             raise ValueError("all tensors must be contiguous device tensors")
         if t.device != x.device:
             raise ValueError("all tensors must be on x's device")
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"x is on {x.device}, and the current device, to which calls go, is cuda:{torch.cuda.current_device()}")
     N, C_in, H, W = x.shape
     C_out, C_in_w, KH, KW = w.shape
     if C_in_w != C_in or scale.numel() != C_out or bias.numel() != C_out:

@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/Exceptions.h>
@@ -48,6 +49,13 @@ const char *name_of(at::ScalarType t) {
         case at::kInt: return "torch.int32";
         default: return "?";
     }
+}
+// A call goes to the current device, whose handle and stream it takes.
+void on_current_device(const at::Tensor &t, const char *what) {
+    const int now = c10::hip::current_device(), its = t.device().index();
+    if (its != now)
+        refuse(PyExc_ValueError, std::string(what) + " is on cuda:" + std::to_string(its) + ", and the current device is cuda:" +
+                                     std::to_string(now));
 }
 using Types = std::initializer_list<at::ScalarType>;
 constexpr at::ScalarType kValues[] = {at::kFloat, at::kBFloat16, at::kHalf};
@@ -120,6 +128,7 @@ template <typename F> PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F &&f) {
 PyObject *int8_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 7, [&]() -> PyObject * {
         const at::Tensor &x = tensor(a[1], "x", kValueTypes);
+        on_current_device(x, "x");
         const at::Tensor &w = tensor(a[2], "w", {at::kChar}, &x);
         const at::Tensor &ws = tensor(a[3], "w_scale", {at::kFloat}, &x);
         if (x.dim() < 1 || w.dim() != 2 || x.size(-1) != w.size(1)) refuse(PyExc_ValueError, "x must be [..., K] and w [N, K]");
@@ -166,6 +175,7 @@ constexpr const char *kCapsule = "conv_bn_silu_amd.cache";
 const Record &record(PyObject *o) {
     const Record *r = (const Record *)PyCapsule_GetPointer(o, kCapsule);
     if (!r) throw Refused();
+    on_current_device(r->k, "the cache");
     if (!r->holds()) refuse(PyExc_ValueError, "the cache's tensors have been given other memory: make a PagedCache of them");
     return *r;
 }
@@ -258,8 +268,8 @@ PyObject *cache_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 9, [&]() -> PyObject * {
         const at::Tensor &q = tensor(a[1], "q", {at::kBFloat16, at::kHalf});
+        on_current_device(q, "q");
         const Record &r = record(a[2]);
-        if (r.k.device() != q.device()) refuse(PyExc_ValueError, "the cache is on another device");
         if (r.k.scalar_type() != at::kChar && r.k.scalar_type() != q.scalar_type())
             refuse(PyExc_TypeError, "the cache must be int8 or of q's type");
         if (q.dim() != 3 || q.size(2) != r.c.dim || r.c.heads < 1 || q.size(1) % r.c.heads || q.size(1) == 0 || q.stride(2) != 1)

@@ -74,3 +74,35 @@ def test_a_cache_keeps_its_tensors(ops):
                 with pytest.raises(ValueError, match="other memory"):
                     call()
             del old
+
+
+def test_conv_on_another_device(monkeypatch):
+    """Calls take the current device's handle and stream, and so tensors that lie there."""
+    from conv_bn_silu_amd import binding as B
+    x, w, s = torch.ones(1, 4, 8, 8, device="cuda"), torch.ones(4, 4, 1, 1, device="cuda"), torch.ones(4, device="cuda")
+    B.conv_bn_silu(x, w, s, s)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (B.conv_bn_silu, B.conv_bn_silu_unfused, B.conv_bn_silu_unfused_noalloc):
+        with pytest.raises(ValueError, match="current device"):
+            call(x, w, s, s)
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second device")
+def test_tensors_of_another_device(ops):
+    def on(d):
+        dev = dict(device=f"cuda:{d}")
+        i32 = dict(dtype=torch.int32, **dev)
+        x = torch.zeros(1, 2, 64, dtype=BF16, **dev)
+        cache = torch.zeros(4, 2, 16, 64, dtype=BF16, **dev)
+        return (lambda: ops.int8_linear(x, torch.zeros(8, 64, dtype=I8, **dev), torch.zeros(8, **dev)),
+                lambda c: ops.cache_write(c, x, x, torch.zeros(1, **i32)), lambda c: ops.cache_read(c, torch.zeros(1, **i32)),
+                lambda c: ops.paged_attention(x, c, torch.zeros(1, 1, **i32), torch.tensor([0, 1], **i32), torch.ones(1, **i32)),
+                cache)
+
+    linear, *calls, k = on(1)
+    with pytest.raises(ValueError, match="current device"):
+        linear()
+    cache = ops.PagedCache(k, k.clone())
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call(cache)
