@@ -6,7 +6,7 @@ Every step runs in the HIP kernels, on the current stream, and PyTorch supplies
 memory (outputs and workspaces come from its allocator) and streams.  The
 arguments are marshalled natively (``csrc/py_block8.cpp``, built into
 ``_block8.so``): a call costs the host little more than its launches.  Forward
-only: the operators are for serving and refuse inputs that require gradients.
+only: the operators are for serving and refuse inputs that require gradients or carry tangents.
 """
 from __future__ import annotations
 

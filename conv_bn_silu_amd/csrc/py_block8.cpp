@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/DynamicTypes.h>
@@ -72,10 +73,12 @@ const at::Tensor &tensor(PyObject *o, const char *what, Types types, const at::T
         refuse(PyExc_TypeError, s);
     }
     const at::Tensor &t = THPVariable_Unpack(o);
-    if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(what) + " must be a device tensor");
-    if (beside && t.device() != beside->device()) refuse(PyExc_ValueError, std::string(what) + " is on another device");
     if (t.requires_grad() && at::GradMode::is_enabled())
         refuse(PyExc_ValueError, std::string(what) + " requires a gradient: these operators are forward only");
+    if (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
+        refuse(PyExc_ValueError, std::string(what) + " carries a tangent: these operators are forward only");
+    if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(what) + " must be a device tensor");
+    if (beside && t.device() != beside->device()) refuse(PyExc_ValueError, std::string(what) + " is on another device");
     return t;
 }
 void contiguous(const at::Tensor &t, at::IntArrayRef shape, const char *what) {

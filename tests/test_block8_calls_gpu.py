@@ -106,3 +106,21 @@ def test_tensors_of_another_device(ops):
     for call in calls:
         with pytest.raises(ValueError, match="current device"):
             call(cache)
+
+
+def test_tangents_are_refused(ops):
+    from torch.autograd import forward_ad
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x, w, s = torch.zeros(2, 64, device="cuda"), torch.zeros(8, 64, dtype=I8, device="cuda"), torch.zeros(8, device="cuda")
+    cache, slots = ops.PagedCache.empty(4, 2, 16, 64, BF16), torch.zeros(1, **i32)
+    k = torch.zeros(1, 2, 64, dtype=BF16, device="cuda")
+    with forward_ad.dual_level():
+        def dual(t):
+            return forward_ad.make_dual(t, torch.ones_like(t))
+        for call in (lambda: ops.int8_linear(dual(x), w, s), lambda: ops.int8_linear(x, w, dual(s)),
+                     lambda: ops.int8_linear(x, w, s, bias=dual(s)), lambda: ops.cache_write(cache, k, dual(k), slots),
+                     lambda: ops.paged_attention(dual(k), cache, torch.zeros(1, 1, **i32), torch.tensor([0, 1], **i32),
+                                                 torch.ones(1, **i32))):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+    assert tuple(ops.int8_linear(x, w, s).shape) == (2, 8)
