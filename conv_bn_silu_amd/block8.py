@@ -15,7 +15,12 @@ import ctypes
 import torch
 
 from .binding import CbsError, Library, default_library, lib
-from . import _block8
+
+try:
+    from . import _block8
+except ImportError as e:
+    raise ImportError("_block8.so is not built, or not for this PyTorch; run __graft_entry__.build() or "
+                      "python conv_bn_silu_amd/build.py") from e
 
 ACTIVATIONS = {None: 0, "silu": 1}
 

@@ -15,8 +15,10 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import re
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -74,10 +76,27 @@ def _compile(src: str, extra: list[str]) -> tuple[str, list[dict]]:
     return obj, parse_resources(res.stderr)
 
 
-def build_module() -> str:
-    """The Python module: host code only, against PyTorch's headers and the library."""
+def _module_needs() -> tuple[str, list[str]]:
+    """PyTorch's folder, and what of the module's needs is not there."""
+    spec = importlib.util.find_spec("torch")
+    root = os.path.dirname(spec.origin) if spec and spec.origin else ""
+    needs = {"PyTorch with its headers": os.path.join(root, "include", "ATen", "core", "Tensor.h"),
+             "Python's headers": os.path.join(sysconfig.get_paths()["include"], "Python.h")}
+    missing = [what for what, path in needs.items() if not os.path.exists(path)]
+    return root, missing + ([] if shutil.which("g++") else ["g++"])
+
+
+def build_module() -> str | None:
+    """The Python module: host code only, against PyTorch's headers and the library.  Where those or
+    g++ are absent there is none (and the library, which needs neither, is whole without it): then
+    the 8-bit block operators are reached through the C ABI only, and importing ``block8`` fails."""
+    root, missing = _module_needs()
+    if missing:
+        if os.path.exists(MODULE):
+            os.remove(MODULE)  # of another build of the library
+        sys.stderr.write(f"{os.path.basename(MODULE)} is not built: {', '.join(missing)} not found\n")
+        return None
     import torch
-    root = os.path.dirname(torch.__file__)
     tmp = MODULE + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
