@@ -121,7 +121,7 @@ int cbs_int8_linear(conv_bn_silu_t h, const void *x, int64_t x_stride, const int
     if (rc != CBS_OK) return rc;
     (void)hipGetLastError();
     const cbs::LinearArgs a{x, x_stride, w, w_scale, bias, y, (int)M, (int)N, (int)K, dtype, activation, workspace};
-    return cbs::record_hip(cbs::launch_int8_linear(a, h->num_cu, (hipStream_t)stream));
+    return cbs::record_hip(cbs::launch_int8_linear(a, (hipStream_t)stream));
 }
 
 int cbs_cache_write(conv_bn_silu_t h, const cbs_paged_cache *cache, const void *k, int64_t k_token_stride,

@@ -40,7 +40,7 @@ struct LinearArgs {
     void *workspace;
 };
 int64_t linear_workspace(int64_t M, int64_t N, int64_t K);
-hipError_t launch_int8_linear(const LinearArgs &a, int num_cu, hipStream_t st);
+hipError_t launch_int8_linear(const LinearArgs &a, hipStream_t st);
 
 struct CacheIo {
     cbs_paged_cache cache;

@@ -504,7 +504,8 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64)) void linear_ring
 
 // --- choice ----------------------------------------------------------------------
 
-// By the number of tiles that a kernel makes of the output, against the 256 CUs.  Where
+// By the number of tiles that a kernel makes of the output, against the CUs of the whole GPU: a constant,
+// for the workspace, which depends on the choice, is asked for without a handle.  Where
 // the choice changes, measured at K 2048 and 8192, in us (ring 64 with K whole; divided below):
 //   M x N         linear_stream   ring 64       ring 128      tile 256
 //   64 x 4096     10.0, 19.9      11.8, 24.2
@@ -514,6 +515,7 @@ __global__ __launch_bounds__(64 * (BM / (32 * MB)) * (BN / 64)) void linear_ring
 //   32 x 8192     10.9, 22.1      12.0, 23.2
 //   32 x 16384    13.5, 37.9      12.9, 28.3
 //   2048 x 8192   (K 4096)        117           86.3          70.4
+constexpr int64_t kCus = 256;
 enum Kind { kStream, kRing64, kRing128, kTile256 };
 // Rows of the fused form for M rows of x, 0 where it does not serve them.
 int fused_rows(int64_t M, int64_t K) {
@@ -526,10 +528,10 @@ Kind kind_of(int64_t M, int64_t N, int64_t K) {
     if (fused_rows(M, K)) return kStream;
     // rows of w that start at odd bytes are read by linear_stream as they are, and have to be copied for the others
     if (K % 16 != 0 && M <= 128) return kStream;
-    if (tiles(M, N, 256) >= 192) return kTile256;
-    if (tiles(M, N, 128) >= 160) return kRing128;
+    if (tiles(M, N, 256) >= kCus * 3 / 4) return kTile256;
+    if (tiles(M, N, 128) >= kCus * 5 / 8) return kRing128;
     if (M > 32 && K > 6144) return kRing64;  // which divides K
-    return tiles(M, N, 64) >= (M <= 32 ? 256 : 96) ? kRing64 : kStream;
+    return tiles(M, N, 64) >= (M <= 32 ? kCus : kCus * 3 / 8) ? kRing64 : kStream;
 }
 // Workgroups of ring 64 that divide K: as many as leave one to a CU, with 16 steps for each, for
 // bringing the sums together takes as long as about 16.  Whole and divided, us:
@@ -541,7 +543,7 @@ Kind kind_of(int64_t M, int64_t N, int64_t K) {
 // (64 x 1024 whole is linear_stream.)
 int splits_of(int64_t M, int64_t N, int64_t K) {
     if (kind_of(M, N, K) != kRing64) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(256 / tiles(M, N, 64), (K + 127) / 128 / 16));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kCus / tiles(M, N, 64), (K + 127) / 128 / 16));
 }
 bool needs_copy(int64_t M, int64_t N, int64_t K) { return K % 16 != 0 && kind_of(M, N, K) != kStream; }
 
@@ -559,7 +561,7 @@ template <typename T, int MT, int NT, int ROWS> hipError_t launch_stream4(Stream
 }
 template <typename T, int MT, int ROWS> hipError_t launch_stream3(const StreamParams &p, hipStream_t st) {
     // 32 rows of w to a workgroup where that leaves two for every CU, else 16
-    const bool two = (int64_t)((p.N + 31) / 32) * ((p.M + 16 * MT - 1) / (16 * MT)) >= 512;
+    const bool two = (int64_t)((p.N + 31) / 32) * ((p.M + 16 * MT - 1) / (16 * MT)) >= 2 * kCus;
     return two ? launch_stream4<T, MT, 2, ROWS>(p, st) : launch_stream4<T, MT, 1, ROWS>(p, st);
 }
 template <typename T> hipError_t launch_stream(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
@@ -615,8 +617,7 @@ int64_t linear_workspace(int64_t M, int64_t N, int64_t K) {
     return l.bytes + (needs_copy(M, N, K) ? N * l.Kp : 0) + (splits > 1 ? tiles(M, N, 64) * (splits * 16384 + 4) : 0);
 }
 
-hipError_t launch_int8_linear(const LinearArgs &a, int num_cu, hipStream_t st) {
-    (void)num_cu;
+hipError_t launch_int8_linear(const LinearArgs &a, hipStream_t st) {
     const CodesLayout l = codes_layout(a.workspace, a.M, a.K);
     switch (a.dtype) {
         case CBS_DTYPE_F32: return launch1<float>(a, l, st);
