@@ -204,9 +204,11 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                 }
             // this tile's scales and values to LDS, the next tile's on their way
             float unit = 0.f;
+            bool uneven = false;
             if constexpr (S::kI8) {
                 const uint32_t bits = magnitude(vs);
                 unit = units.of_tile(bits, ((valid >> (lane % KT)) & 1) && bits < 0x7F800000u);
+                uneven = __builtin_amdgcn_readfirstlane(__float_as_int(unit)) == __builtin_bit_cast(int, kUneven);
                 kscale[lane % KT] = finite_or_nan(ks);
                 vscale[lane % KT] = in_unit(vs, unit);
             }
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                 if constexpr (S::kI8) {
                     const float x = top * qf[i];
                     float u = x + unit;
-                    if (unit == kUneven) {
+                    if (uneven) {
                         u = -INFINITY;
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb) {
@@ -283,15 +285,17 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                         u = fmaxf(u, __shfl_xor(u, 16, 64));
                         u = fmaxf(u, __shfl_xor(u, 32, 64));
                     }
-                    const float now = x > m[i] + kSlack ? x : m[i], now_o = product_exponent(mo[i], u);
-                    if (__any(now != m[i] || now_o != mo[i])) {
+                    if (__any(x > m[i] + kSlack || u > mo[i] + (kSlack + kLift))) {
+                        const float now = x > m[i] + kSlack ? x : m[i], now_o = product_exponent(mo[i], u);
                         l[i] *= __builtin_amdgcn_exp2f(m[i] - now);
                         const float fade = __builtin_amdgcn_exp2f(mo[i] - now_o);
                         m[i] = now, mo[i] = now_o;
 #pragma unroll
                         for (int d = 0; d < S::kDims / 16; ++d) o[i][d] *= fade;
                     }
-                    if (unit == kUneven) {
+                    base = tile_exponent(m[i], mo[i], unit);
+                    if (uneven) {
+                        base = m[i];
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb) {
                             __builtin_amdgcn_sched_barrier(0);
@@ -300,7 +304,6 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
                             for (int e = 0; e < 4; ++e) vsc[kb][e] = uneven_scale(vsc[kb][e], m[i], mo[i]);
                         }
                     }
-                    base = tile_exponent(m[i], mo[i], unit);
                     to_sum = __builtin_amdgcn_exp2f(base - m[i]);
                 } else {
                     const bool move = top > m[i] && !((top - m[i]) * qf[i] <= kSlack);

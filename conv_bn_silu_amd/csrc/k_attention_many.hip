@@ -351,27 +351,29 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
                 const float unit = units[buf][part], x = top * qf;
 #pragma unroll
                 for (int g = 0; g < 8; ++g) per_key[g] = *(const f32x4 *)(&vscale[buf][KT * part + 8 * g + 4 * half]);
+                const bool uneven = __builtin_amdgcn_readfirstlane(__float_as_int(unit)) == __builtin_bit_cast(int, kUneven);
                 float u = x + unit;
-                if (__builtin_expect(__any(unit == kUneven), 0)) {
+                if (__builtin_expect(uneven, 0)) {
                     u = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         u = fmaxf(u, __builtin_fmaf(s[i / 16][i % 16], qf, __builtin_amdgcn_logf(fabsf(per_key[i / 4][i % 4]))));
                     u = max_halves(u);
                 }
-                const float now = x > m + kSlack ? x : m, now_o = product_exponent(mo, u);
-                if (__any(now != m || now_o != mo)) {
+                if (__any(x > m + kSlack || u > mo + (kSlack + kLift))) {
+                    const float now = x > m + kSlack ? x : m, now_o = product_exponent(mo, u);
                     l *= __builtin_amdgcn_exp2f(m - now);
                     const float fade = __builtin_amdgcn_exp2f(mo - now_o);
                     m = now, mo = now_o;
 #pragma unroll
                     for (int db = 0; db < NB; ++db) o[db] *= fade;
                 }
-                if (__builtin_expect(__any(unit == kUneven), 0)) {
+                base = tile_exponent(m, mo, unit);
+                if (__builtin_expect(uneven, 0)) {
+                    base = m;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) per_key[i / 4][i % 4] = uneven_scale(per_key[i / 4][i % 4], m, mo);
                 }
-                base = tile_exponent(m, mo, unit);
                 to_sum = __builtin_amdgcn_exp2f(base - m);
             } else {
                 const bool move = top > m && !((top - m) * qf <= kSlack);
