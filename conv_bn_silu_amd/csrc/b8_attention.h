@@ -11,6 +11,12 @@
 // at the end.  The probabilities are then, as they stand, the operand of
 // O^T = V^T P^T, whose result again has one query to a lane.
 //
+// Bits.  Scores, maxima, sums and outputs are fp32.  What meets in a matrix instruction has 16 bits,
+// for those of fp32 take 16 times as long: the probabilities are rounded to the cache's type (bf16 or
+// fp16; fp16 for 8-bit codes), off by half a step of it each, while the sum adds them unrounded.  That shows: the error of
+// the outputs against 64 bits is 0.0021 of their size where rounding the outputs alone would leave
+// 0.0016 (bf16), 0.0003 and 0.0002 (fp16).
+//
 // Units.  t = q . k (times the key's scale), x = c t the exponent of two, with
 // c = |scale| log2 e and the scale's sign put into q.  The running maximum m is
 // one of t; a probability is 2^(c t - c m).  m moves only where a score passes it

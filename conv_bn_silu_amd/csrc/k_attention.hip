@@ -120,7 +120,10 @@ int64_t make_plan(AttentionPlan &p, int64_t batch, int64_t tokens, int64_t heads
     // 32 rows only where the average sequence has more than 16: the registers they take cost
     // waves (8 sequences of 2 tokens, groups of 4, over 3000 keys: 41 us, with 16 rows 25)
     p.few.tile = dim <= 128 && tokens * group > 16 * batch ? 32 : 16;
-    // with no more tokens than sequences they are single tokens, as a rule
+    // With no more tokens than sequences they are single tokens, as a rule, and a launch of attend_many that
+    // finds nothing would cost 4 of 10 us.  A batch padded with empty sequences breaks the rule, and its chunk
+    // goes 32 rows at a time (60 tokens after 4000, 32 heads over 8, us: alone 28, with 58 empty sequences beside
+    // it, which still is attend_many, 52, with 63 269).
     p.few_only = tokens <= batch || tokens * group <= p.few.tile;
     // Two waves to a row where tiles of 256 rows leave CUs idle and a tile's keys are not many times
     // its tokens (then chunks fill the CUs as well).  One and two, us: a prompt of 1000 49.4 and

@@ -12,9 +12,10 @@
 // instructions as they are; values pass through a piece of LDS that only the wave uses, and
 // come back transposed.  No barrier in the loop.
 //
-// Bound by HBM: 64 sequences of 2000 to 16000 keys, 32 heads over 8, dim 128, 8 bits: 232 us a
-// call, 5.2 TB/s (16 bits: 415 us, 5.6 TB/s; a large copy reaches 4.8).  The matrix pipe is 7%
-// busy, though 12 of its 16 columns are padding there, and the vector pipe 56%: what
+// Bound by HBM: 64 sequences of 2000 to 16000 keys, 32 heads over 8, dim 128, 8 bits: 244 us a
+// call, 5.0 TB/s (16 bits: 428 us, 5.5 TB/s; a large copy reaches 6.3; dim 256: 521 and 839 us).  Value
+// scales that differ by more than 2^7 within 64 keys cost 20 us of 244.  The matrix pipe is 7%
+// busy, though 12 of its 16 columns are padding there, and the vector pipe 49%: what
 // unpacks the codes and the softmax hides under the loads.
 #include <hip/hip_runtime.h>
 

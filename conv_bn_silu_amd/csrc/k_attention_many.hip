@@ -9,9 +9,10 @@
 // their way, and the page numbers of the one after.  A wave's scores never
 // leave its registers.
 //
-// Bound by the issue of vector and matrix instructions, which hardly overlap (57% and 34% of
-// a SIMD's cycles), and by power: 2 prompts of 8192, 32 heads over 8, dim 128, 8 bits: 1310
-// us, 0.84 PFLOP/s; a large library product reaches 1.13.
+// Bound by the issue of vector and matrix instructions, which hardly overlap (60% and 37% of
+// a SIMD's cycles), and by power: 2 prompts of 8192, 32 heads over 8, dim 128, 8 bits: 1280
+// us, 0.86 PFLOP/s; a large library product reaches 1.2.  Value scales that differ by more than 2^7
+// within 64 keys, all along: 1725.
 #include <hip/hip_runtime.h>
 
 #include "b8_attention.h"
@@ -29,11 +30,11 @@ template <typename C, int NB, int SPLIT> struct ManyShape {
     static constexpr bool kI8 = std::is_same_v<C, int8_t>;
     // Dim 256 needs the registers of two waves; 16-bit caches at dim 64 need so few that three
     // waves fit a SIMD (2 prompts of 6000: 8 waves 469 us, 12 waves 407; with 8-bit
-    // caches 543 and 593, for there it takes scratch memory or 168 registers of 196).
+    // caches 543 and 593, for there it takes scratch memory or 168 registers of 192).
     static constexpr int kWaves = NB > 4 ? 4 : NB == 2 && !kI8 && SPLIT == 1 ? 12 : 8;
     // A wave at its step goes before one that stages the next (2 prompts of 8192, 8 bits, 1317 ->
-    // 1302 us; 2 of 6000, 16 bits, 699 -> 689, dim 64 412 -> 401; 8 bits at dim 64 530 -> 546, dim
-    // 256 511 -> 514).
+    // 1302 us; 2 of 6000, 16 bits, 699 -> 689, dim 64 412 -> 401; 8 bits at dim 64 533 -> 551, dim
+    // 256 2085 -> 2098).
     static constexpr bool kStepFirst = NB <= 4 && (NB > 2 || !kI8);
     static constexpr int kGroups = kWaves / SPLIT;  // waves with rows of their own
     static constexpr int kThreads = 64 * kWaves, kTile = 32 * kGroups, KS = KT * SPLIT;

@@ -9,13 +9,16 @@
 // pipe is the bound.  The sums are 32-bit integers and so the same whatever the order; where
 // few tiles have long sums, several workgroups of linear_ring divide a tile's K.
 //
-// Measured, us a call with the pass that quantises x (copying at 4.8 TB/s, matrix
-// products at 2.03 POP/s would take the second figure):
-//   1 x 4096 x 4096      stream     7.2   3.5      256 x 4096 x 4096     ring 64    16   4.4
-//   1 x 16384 x 4096     stream    14.7  14.0      1024 x 4096 x 4096    ring 128   30    17
-//   40 x 16384 x 4096    ring 64   17.0  14.3      4096 x 4096 x 4096    tile       76    68
-//   128 x 16384 x 4096   ring 64   21.2  15.1      8192 x 8192 x 8192    tile      525   541
-//   128 x 1024 x 8192    4 parts   16.7   2.2
+// Measured, us a call with the pass that quantises x (copying at 6.3 TB/s, matrix
+// products at 2.1 POP/s would take the second figure):
+//   1 x 4096 x 4096      stream     6.6   2.7      256 x 4096 x 4096     ring 64    18   4.1
+//   1 x 16384 x 4096     stream    15.3  10.7      1024 x 4096 x 4096    ring 128   33    16
+//   40 x 16384 x 4096    ring 64   18.7  10.9      4096 x 4096 x 4096    tile       81    65
+//   128 x 16384 x 4096   ring 64   22.9  11.5      8192 x 8192 x 8192    tile      529   524
+//   128 x 1024 x 8192    4 parts   17.3   1.7
+// The pass over x takes 4 us of it for few rows, 5 to 8 for 256 to 1024 and 47 for 8192 x 8192.
+// 1024 x 4096 x 4096 has 256 tiles of 128, one to a CU: 25 us for 32 steps with four waves to feed a CU's matrix
+// pipes, where 256-tiles (64 of them) would leave three CUs of four idle.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

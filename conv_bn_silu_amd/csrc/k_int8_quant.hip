@@ -8,7 +8,7 @@
 // Bound by HBM (reads e M K bytes, writes M K).  A row is held in registers
 // between finding its largest magnitude and quantising it, 32 values a lane:
 // one wave per row up to K = 2048, a workgroup of four waves beyond; rows longer
-// than 8192 are read a second time (from L2).  8192 x 8192 bf16: 47 us, 4.2 TB/s; a
+// than 8192 are read a second time (from L2).  8192 x 8192 bf16: 47 to 50 us, 4.2 TB/s; a
 // few rows: 4 us, the latency of one pass.
 #include <hip/hip_runtime.h>
 
