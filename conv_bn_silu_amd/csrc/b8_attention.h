@@ -73,7 +73,10 @@ int many_tile(int64_t dim, bool int8, bool split);  // rows of its tile
 #ifdef __HIPCC__
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;  // of the running maximum, as an exponent of two
-constexpr float kLift = 6.f;   // of the products with an 8-bit value's scale, which 2^(8 + 6) keeps within fp16
+// fp16 holds 2^(8 + 6): what meets the values in it is 2^6 times as large as the unit says, so that
+// less is lost at its lower end, which small probabilities of large values reach.
+constexpr float kLift = 6.f;
+template <typename X> constexpr float kLiftOf = std::is_same_v<X, _Float16> ? kLift : 0.f;
 
 struct Sequence {
     int b, first, n, len;  // its rows of q and the tokens it has in the cache

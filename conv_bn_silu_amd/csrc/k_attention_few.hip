@@ -316,7 +316,7 @@ __global__ __launch_bounds__(kThreads, (FewShape<C, ND, QT>::kPerSimd)) void att
 #pragma unroll
                         for (int d = 0; d < S::kDims / 16; ++d) o[i][d] *= fade;
                     }
-                    base = m[i] == -INFINITY ? 0.f : m[i] * qf[i];
+                    base = m[i] == -INFINITY ? 0.f : __builtin_fmaf(m[i], qf[i], -kLiftOf<X>);
                 }
                 float sum = 0.f;
 #pragma unroll

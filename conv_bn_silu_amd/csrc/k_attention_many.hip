@@ -386,7 +386,7 @@ __global__ __launch_bounds__((ManyShape<C, NB, SPLIT>::kThreads), (ManyShape<C, 
 #pragma unroll
                     for (int db = 0; db < NB; ++db) o[db] *= fade;
                 }
-                base = m == -INFINITY ? 0.f : m * qf;
+                base = m == -INFINITY ? 0.f : __builtin_fmaf(m, qf, -kLiftOf<X>);
             }
             // values: keys 16 t + 4 half + 0..3 and 8 above those, of dim 32 db + col
             auto read_v = [&](int i) {

@@ -35,9 +35,10 @@ def expect(c):
     return ref, O.rounded(ref, tol + small_products(c), c["q"].dtype)
 
 
-def small_products(c):
+def for_each_row(c, lost):
+    """lost(p, pages, head, offsets) for the keys that a token sees, p their probabilities for each head of a group."""
     table, page = c["table"].long(), c["tensors"][0].shape[2]
-    k, s = c["kv64"][0], c["tensors"][3].double().nan_to_num(0)
+    k = c["kv64"][0]
     heads, hk = c["q"].shape[1], k.shape[1]
     out = torch.zeros(c["q"].shape, dtype=O.F64)
     for b, n in enumerate(c["lens"]):
@@ -49,9 +50,13 @@ def small_products(c):
             for h in range(hk):
                 mine = slice(h * heads // hk, (h + 1) * heads // hk)
                 z = c["q"][at, mine].double() @ k[pages, h, j % page][seen].t() * c["scale"]
-                top = (torch.softmax(z, -1) * s.abs()[pages, h, j % page][seen]).amax(-1)
-                out[at, mine] = (127 * int(seen.sum()) * 2.0 ** -24 * top)[:, None]
+                out[at, mine] = lost(torch.softmax(z, -1), pages[seen], h, (j % page)[seen])[:, None]
     return out
+
+
+def small_products(c):
+    s = c["tensors"][3].double().nan_to_num(0).abs()
+    return for_each_row(c, lambda p, pages, h, off: 127 * p.shape[1] * 2.0 ** -24 * (p * s[pages, h, off]).amax(-1))
 
 
 def check(ops, c, what):
@@ -152,3 +157,29 @@ def test_scales_of_every_size(ops, call):
     c = attention_case(new, lens, heads, hk, dim, 16, BF16, True, seed=54)
     c["tensors"][3][:, :, ::3] *= -3
     check(ops, c, f"{call} negative")
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_small_weights_of_large_values(ops, call):
+    """fp16 caches: keys of a weight of 2^-24 to 2^-28 with values of thousands, beside ones of thousandths.
+
+    The largest probability is 2^6 or more in the unit in which they become fp16, which is off by up to 2^-25: for
+    each key 2^-31 of the largest probability, times the largest value."""
+    new, lens, heads, hk, dim = CALLS[call]
+    c = attention_case(new, lens, heads, hk, dim, 16, F16, False, seed=55)
+    g = torch.Generator().manual_seed(55)
+    c["q"] = torch.ones_like(c["q"])
+    k, v = c["tensors"]
+    live = ~k[..., :1].isnan()
+    far = (torch.rand(live.shape, generator=g) < 0.3) & live
+    score = torch.where(far, -17 - 2.5 * torch.rand(live.shape, generator=g), 0.0)
+    value = torch.randn(v.shape, generator=g)
+    k.copy_(torch.where(live, (score * dim ** -0.5).expand_as(k), math.nan))
+    v.copy_(torch.where(live, torch.where(far, 8000 * value.clamp(-4, 4), 1e-3 * value), math.nan))
+    c["kv64"] = tuple(torch.where(live, t.double(), 0.0) for t in (k, v))
+    ref, _, _ = O.attention(c["q"], *c["kv64"], c["table"], c["starts"], c["lens"], 0, c["scale"], 0.0)
+    _, tol, _ = O.attention(c["q"].double(), *c["kv64"], c["table"], c["starts"], c["lens"], 0, c["scale"],
+                            O.half_step(F16) * (1 + 2.0 ** -30))
+    tol = tol + for_each_row(c, lambda p, pages, h, off: p.shape[1] * 2.0 ** -31 * p.amax(-1) * c["kv64"][1][pages, h, off].abs().amax())
+    say("[value range]", call, "small weights")
+    O.check(run_case(ops, c), ref, O.rounded(ref, tol, F16), call)
