@@ -219,7 +219,7 @@ constexpr float kNoExponent = -3.4028235e38f;
 // mo after a tile whose largest product has the exponent u.
 __device__ __forceinline__ float product_exponent(float mo, float u) { return u > mo + (kSlack + kLift) ? u - kLift : mo; }
 // The exponent that an even tile's probabilities are taken relative to (an uneven one's: m).  Where it is kFar above m the
-// products are nothing in fp16 (below 2^-46), while the sum still gets what the row sees.
+// products are nothing in fp16 (below 2^-52), while the sum still gets what the row sees.
 constexpr float kFar = 60.f;
 __device__ __forceinline__ float tile_exponent(float m, float mo, float unit) {
     return fminf(mo - unit, m + kFar);
