@@ -11,6 +11,7 @@ only: the operators are for serving and refuse inputs that require gradients or 
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -25,8 +26,8 @@ except ImportError as e:
 ACTIVATIONS = {None: 0, "silu": 1}
 
 # Every function include/cbs_block8.h declares.
-EXPORTS = ["cbs_int8_linear", "cbs_int8_linear_workspace", "cbs_cache_write", "cbs_cache_read", "cbs_paged_attention",
-           "cbs_paged_attention_workspace"]
+EXPORTS = ["cbs_int8_linear", "cbs_int8_linear_workspace", "cbs_int8_linear_rows", "cbs_int8_linear_rows_workspace",
+           "cbs_rows8_bytes", "cbs_cache_write", "cbs_cache_read", "cbs_paged_attention", "cbs_paged_attention_workspace"]
 
 
 def _declare():
@@ -35,12 +36,15 @@ def _declare():
     cache = vp
     lib.cbs_int8_linear.argtypes = [vp, vp, l, vp, vp, vp, vp, l, l, l, i, i, vp, l, vp]
     lib.cbs_int8_linear_workspace.argtypes = [l, l, l]
+    lib.cbs_int8_linear_rows.argtypes = [vp, vp, vp, vp, vp, vp, l, l, l, i, i, vp, l, vp]
+    lib.cbs_int8_linear_rows_workspace.argtypes = [l, l, l]
+    lib.cbs_rows8_bytes.argtypes = [l, l]
     lib.cbs_cache_write.argtypes = [vp, cache, vp, l, l, vp, l, l, vp, l, i, vp]
     lib.cbs_cache_read.argtypes = [vp, cache, vp, l, vp, vp, i, vp]
     lib.cbs_paged_attention.argtypes = [vp, vp, l, l, cache, vp, l, l, vp, vp, l, l, i, i, f, vp, i, vp, l, vp]
     lib.cbs_paged_attention_workspace.argtypes = [vp, l, l, i, i, i, i, l]
     for name in EXPORTS:
-        getattr(lib, name).restype = l if name.endswith("_workspace") else i
+        getattr(lib, name).restype = l if name.endswith(("_workspace", "_bytes")) else i
 
 
 _declare()
@@ -63,6 +67,37 @@ def _checked(got, library, what):
     return got
 
 
+class Rows8:
+    """Rows in 8 bits, [..., K]: codes in [-127, 127], each row with a scale, as the linear layer makes
+    them of its input and ``add_rms_norm`` gives them.  They lie as the layer's matrix kernels read them, in
+    one int8 tensor (`buffer`; the layout is in include/cbs_block8.h).  dtype: of what they were made of, and
+    of the layer's output.
+    """
+
+    def __init__(self, buffer, shape, dtype):
+        self.buffer, self.shape, self.dtype = buffer, torch.Size(shape), dtype
+        self._lead, self._k = tuple(self.shape[:-1]), self.shape[-1]
+        self._rows = math.prod(self._lead)
+
+    def _split(self):
+        r = (self._rows + 15) // 16 * 16
+        return self.buffer[:4 * r].view(torch.float32), self.buffer[4 * r:].view((self._k + 127) // 128 * 2, r, 64)
+
+    @property
+    def scale(self):
+        """float32 [...], in the buffer."""
+        return self._split()[0][:self._rows].view(self._lead)
+
+    @property
+    def codes(self):
+        """int8 [..., K], a copy."""
+        return self._split()[1].transpose(0, 1).flatten(1)[:self._rows, :self._k].reshape(self.shape)
+
+    def dequantize(self, dtype=None):
+        """codes * scale, a copy of `dtype` (that of what they were made of by default)."""
+        return (self.codes.float() * self.scale[..., None]).to(dtype or self.dtype)
+
+
 def int8_linear(x, w, w_scale, bias=None, activation=None, out=None, library: Library | None = None):
     """y = act(x @ w.T) in 8-bit integers: the rows of x are quantised with one
     scale a row, multiplied by w exactly, and scaled back.
@@ -70,8 +105,11 @@ def int8_linear(x, w, w_scale, bias=None, activation=None, out=None, library: Li
     x: [..., K] float32, bfloat16 or float16 (rows K apart or further, each
     contiguous, else they are copied); w: int8 [N, K]; w_scale: float32 [N]
     (w * w_scale is the weight); bias: float32 [N] or None; activation: None or
-    "silu".  Returns [..., N] of x's type.
+    "silu".  Returns [..., N] of x's type.  x may be ``Rows8``, quantised already.
     """
+    if type(x) is Rows8:
+        return _checked(_block8.int8_linear_rows(_handle(library), x.buffer, x._rows, x._k, x.dtype, x._lead, w, w_scale, bias,
+                                                 ACTIVATIONS.get(activation, -1), out), library, "cbs_int8_linear_rows")
     return _checked(_block8.int8_linear(_handle(library), x, w, w_scale, bias, ACTIVATIONS.get(activation, -1), out),
                     library, "cbs_int8_linear")
 

@@ -102,7 +102,7 @@ def build_module() -> str | None:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include/torch/csrc/api/include"),
            "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "py_block8.cpp"), "-o", tmp, "-L" + HERE, "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(root, "lib"),
+           *sorted(glob.glob(os.path.join(CSRC, "py_*.cpp"))), "-o", tmp, "-L" + HERE, "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(root, "lib"),
            "-l:libconv_bn_silu.so", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     subprocess.run(cmd, check=True)
     os.replace(tmp, MODULE)

@@ -8,28 +8,16 @@
 #include <cstdint>
 #include <initializer_list>
 
+#include "b8_checks.h"
 #include "b8_launch.h"
 #include "cbs_handle.h"
 
 namespace {
 
-struct Span {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Span span(const void *p, int64_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (uintptr_t)(p ? bytes : 0)}; }
-bool disjoint(Span a, std::initializer_list<Span> others) {
-    for (const Span &o : others)
-        if (a.lo < o.hi && o.lo < a.hi) return false;
-    return true;
-}
-
-bool value_type(int dtype) { return dtype == CBS_DTYPE_F32 || dtype == CBS_DTYPE_BF16 || dtype == CBS_DTYPE_F16; }
-int64_t element(int dtype) { return dtype == CBS_DTYPE_F32 ? 4 : dtype == CBS_DTYPE_I8 ? 1 : 2; }
-bool aligned(const void *p, int64_t to) { return (uintptr_t)p % (uintptr_t)to == 0; }
+using namespace cbs;
 
 constexpr int64_t kMaxK = 131072;          // 128 * 128 * K < 2^31
 constexpr int64_t kMaxRows = 1 << 24;
-constexpr int64_t kMaxStride = 1ll << 40;  // keeps 64-bit offsets exact
 
 int check_linear(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 1 || K < 1) return CBS_ERR_INVALID_ARG;
@@ -37,40 +25,33 @@ int check_linear(int64_t M, int64_t N, int64_t K) {
     return CBS_OK;
 }
 
-// The cache's own fields; its bytes and the spans of its tensors.
-int check_cache(const cbs_paged_cache *c) {
-    if (!c || c->pages < 1 || c->heads < 1 || c->page_size < 1 || c->dim < 1) return CBS_ERR_INVALID_ARG;
-    if (!value_type(c->dtype) && c->dtype != CBS_DTYPE_I8) return CBS_ERR_INVALID_ARG;
-    if (!c->k || !c->v) return CBS_ERR_INVALID_ARG;
-    if (c->dtype == CBS_DTYPE_I8 ? (!c->k_scale || !c->v_scale) : (c->k_scale || c->v_scale)) return CBS_ERR_INVALID_ARG;
-    if (c->pages > INT32_MAX || c->pages * c->page_size > INT32_MAX || c->heads > 65536) return CBS_ERR_UNSUPPORTED;
-    if (c->dim % 8 != 0 || c->dim > 256) return CBS_ERR_UNSUPPORTED;
-    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+// Of x, or of rows in 8 bits.
+int linear(conv_bn_silu_t h, const void *x, int64_t x_stride, const void *rows, const int8_t *w, const float *w_scale,
+           const float *bias, void *y, int64_t M, int64_t N, int64_t K, int dtype, int activation, void *workspace,
+           int64_t workspace_bytes, void *stream) {
+    if (!cbs::handle_live(h)) return CBS_ERR_BAD_HANDLE;
+    if (!value_type(dtype) || (activation != CBS_ACT_NONE && activation != CBS_ACT_SILU)) return CBS_ERR_INVALID_ARG;
+    int rc = check_linear(M, N, K);
+    if (rc != CBS_OK) return rc;
+    if (M == 0) return CBS_OK;
+    if ((!x && !rows) || !w || !w_scale || !y || (x && x_stride < K)) return CBS_ERR_INVALID_ARG;
+    if (x_stride > kMaxStride) return CBS_ERR_UNSUPPORTED;
+    const int64_t e = element(dtype), need = cbs::linear_workspace(M, N, K, rows != nullptr);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return CBS_ERR_INVALID_ARG;
+    const Span sy = span(y, M * N * e), sw = span(workspace, need);
+    const Span in[] = {span(x, ((M - 1) * x_stride + K) * e), span(rows, cbs::rows8_bytes(M, K)), span(w, N * K),
+                       span(w_scale, N * 4), span(bias, N * 4)};
+    for (const Span &i : in)
+        if (!disjoint(i, {sy, sw})) return CBS_ERR_INVALID_ARG;
+    if (!disjoint(sy, {sw})) return CBS_ERR_INVALID_ARG;
+    if (!aligned(x, e) || !aligned(rows, 16) || !aligned(y, e) || !aligned(w_scale, 4) || !aligned(bias, 4) ||
+        !aligned(workspace, 16))
         return CBS_ERR_UNSUPPORTED;
-    return CBS_OK;
-}
-int64_t cache_rows(const cbs_paged_cache &c) { return c.pages * c.heads * c.page_size; }
-int64_t cache_bytes(const cbs_paged_cache &c) { return cache_rows(c) * c.dim * element(c.dtype); }
-bool clear_of_cache(Span s, const cbs_paged_cache &c) {
-    return disjoint(s, {span(c.k, cache_bytes(c)), span(c.v, cache_bytes(c)), span(c.k_scale, cache_rows(c) * 4),
-                        span(c.v_scale, cache_rows(c) * 4)});
-}
-bool tensors_disjoint(const cbs_paged_cache &c) {
-    const Span k = span(c.k, cache_bytes(c)), v = span(c.v, cache_bytes(c));
-    const Span ks = span(c.k_scale, cache_rows(c) * 4), vs = span(c.v_scale, cache_rows(c) * 4);
-    return disjoint(k, {v, ks, vs}) && disjoint(v, {ks, vs}) && disjoint(ks, {vs});
-}
-
-int check_strides(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride, int64_t head_stride) {
-    (void)tokens;
-    if (head_stride < dim && heads > 1) return CBS_ERR_INVALID_ARG;
-    if (token_stride < dim && tokens > 1) return CBS_ERR_INVALID_ARG;
-    if (token_stride < 0 || head_stride < 0) return CBS_ERR_INVALID_ARG;
-    if (token_stride > kMaxStride || head_stride > kMaxStride) return CBS_ERR_UNSUPPORTED;
-    return CBS_OK;
-}
-int64_t strided_bytes(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride, int64_t head_stride, int dtype) {
-    return ((tokens - 1) * token_stride + (heads - 1) * head_stride + dim) * element(dtype);
+    rc = cbs::check_device(h);
+    if (rc != CBS_OK) return rc;
+    (void)hipGetLastError();
+    const cbs::LinearArgs a{x, x_stride, w, w_scale, bias, y, (int)M, (int)N, (int)K, dtype, activation, workspace, rows};
+    return cbs::record_hip(cbs::launch_int8_linear(a, (hipStream_t)stream));
 }
 
 int check_attention_sizes(int64_t batch, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
@@ -95,33 +76,23 @@ int check_attention_sizes(int64_t batch, int64_t tokens, int64_t heads, int64_t 
 extern "C" {
 
 int64_t cbs_int8_linear_workspace(int64_t M, int64_t N, int64_t K) {
-    return check_linear(M, N, K) == CBS_OK ? cbs::linear_workspace(M, N, K) : -1;
+    return check_linear(M, N, K) == CBS_OK ? cbs::linear_workspace(M, N, K, false) : -1;
 }
+int64_t cbs_int8_linear_rows_workspace(int64_t M, int64_t N, int64_t K) {
+    return check_linear(M, N, K) == CBS_OK ? cbs::linear_workspace(M, N, K, true) : -1;
+}
+int64_t cbs_rows8_bytes(int64_t M, int64_t K) { return check_linear(M, 1, K) == CBS_OK ? cbs::rows8_bytes(M, K) : -1; }
 
 int cbs_int8_linear(conv_bn_silu_t h, const void *x, int64_t x_stride, const int8_t *w, const float *w_scale,
                     const float *bias, void *y, int64_t M, int64_t N, int64_t K, int dtype, int activation,
                     void *workspace, int64_t workspace_bytes, void *stream) {
-    if (!cbs::handle_live(h)) return CBS_ERR_BAD_HANDLE;
-    if (!value_type(dtype) || (activation != CBS_ACT_NONE && activation != CBS_ACT_SILU)) return CBS_ERR_INVALID_ARG;
-    int rc = check_linear(M, N, K);
-    if (rc != CBS_OK) return rc;
-    if (M == 0) return CBS_OK;
-    if (!x || !w || !w_scale || !y || x_stride < K) return CBS_ERR_INVALID_ARG;
-    if (x_stride > kMaxStride) return CBS_ERR_UNSUPPORTED;
-    const int64_t e = element(dtype), need = cbs::linear_workspace(M, N, K);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return CBS_ERR_INVALID_ARG;
-    const Span sy = span(y, M * N * e), sw = span(workspace, need);
-    const Span in[] = {span(x, ((M - 1) * x_stride + K) * e), span(w, N * K), span(w_scale, N * 4), span(bias, N * 4)};
-    for (const Span &i : in)
-        if (!disjoint(i, {sy, sw})) return CBS_ERR_INVALID_ARG;
-    if (!disjoint(sy, {sw})) return CBS_ERR_INVALID_ARG;
-    if (!aligned(x, e) || !aligned(y, e) || !aligned(w_scale, 4) || !aligned(bias, 4) || !aligned(workspace, 16))
-        return CBS_ERR_UNSUPPORTED;
-    rc = cbs::check_device(h);
-    if (rc != CBS_OK) return rc;
-    (void)hipGetLastError();
-    const cbs::LinearArgs a{x, x_stride, w, w_scale, bias, y, (int)M, (int)N, (int)K, dtype, activation, workspace};
-    return cbs::record_hip(cbs::launch_int8_linear(a, (hipStream_t)stream));
+    return linear(h, x, x_stride, nullptr, w, w_scale, bias, y, M, N, K, dtype, activation, workspace, workspace_bytes, stream);
+}
+
+int cbs_int8_linear_rows(conv_bn_silu_t h, const void *rows, const int8_t *w, const float *w_scale, const float *bias,
+                         void *y, int64_t M, int64_t N, int64_t K, int dtype, int activation, void *workspace,
+                         int64_t workspace_bytes, void *stream) {
+    return linear(h, nullptr, 0, rows, w, w_scale, bias, y, M, N, K, dtype, activation, workspace, workspace_bytes, stream);
 }
 
 int cbs_cache_write(conv_bn_silu_t h, const cbs_paged_cache *cache, const void *k, int64_t k_token_stride,

@@ -38,8 +38,10 @@ struct LinearArgs {
     void *y;
     int M, N, K, dtype, act;
     void *workspace;
+    const void *rows;  // in 8 bits already, in place of x; else null
 };
-int64_t linear_workspace(int64_t M, int64_t N, int64_t K);
+int64_t linear_workspace(int64_t M, int64_t N, int64_t K, bool rows);  // rows: given in 8 bits
+int64_t rows8_bytes(int64_t M, int64_t K);
 hipError_t launch_int8_linear(const LinearArgs &a, hipStream_t st);
 
 struct CacheIo {

@@ -569,14 +569,14 @@ template <typename T, int MT, int ROWS> hipError_t launch_stream3(const StreamPa
 }
 template <typename T> hipError_t launch_stream(const LinearArgs &a, const CodesLayout &l, hipStream_t st) {
     const StreamParams p{l, a.w, a.w_scale, a.bias, a.x, a.x_stride, a.y, a.M, a.N, a.K, a.dtype, a.act, 0};
-    switch (fused_rows(a.M, a.K)) {
+    if (!a.rows) switch (fused_rows(a.M, a.K)) {
         case 1: return launch_stream3<T, 1, 1>(p, st);
         case 2: return launch_stream3<T, 1, 2>(p, st);
         case 4: return launch_stream3<T, 1, 4>(p, st);
         case 8: return launch_stream3<T, 1, 8>(p, st);
         case 16: return launch_stream3<T, 1, 16>(p, st);
     }
-    const hipError_t e = launch_quant_rows(a, l, nullptr, nullptr, 0, st);
+    const hipError_t e = a.rows ? hipSuccess : launch_quant_rows(a, l, nullptr, nullptr, 0, st);
     if (e != hipSuccess) return e;
     // from here on x is not read: one type of the kernel serves all
     if (a.M <= 16) return launch_stream3<float, 1, 0>(p, st);
@@ -594,10 +594,13 @@ template <typename T, bool SILU> hipError_t launch2(const LinearArgs &a, const C
     const int steps = l.Kp / 128, splits = splits_of(a.M, a.N, a.K), count = (int)tiles(a.M, a.N, 64);
     p.split_steps = (steps + splits - 1) / splits;
     p.splits = (steps + p.split_steps - 1) / p.split_steps;
-    int8_t *const to = copy ? l.codes + (int64_t)l.rows * l.Kp : nullptr;
-    p.sums = (int *)(l.codes + (int64_t)l.rows * l.Kp + (copy ? (int64_t)a.N * l.Kp : 0));
+    int8_t *const beside = a.rows ? (int8_t *)a.workspace : l.codes + (int64_t)l.rows * l.Kp, *const to = copy ? beside : nullptr;
+    p.sums = (int *)(beside + (copy ? (int64_t)a.N * l.Kp : 0));
     p.arrived = p.sums + (int64_t)splits * count * 4096;
-    const hipError_t e = launch_quant_rows(a, l, to, p.splits > 1 ? p.arrived : nullptr, count, st);
+    int *const zeros = p.splits > 1 ? p.arrived : nullptr;
+    hipError_t e = hipSuccess;
+    if (!a.rows) e = launch_quant_rows(a, l, to, zeros, count, st);
+    else if (to || zeros) e = launch_beside_rows(a, l, to, zeros, count, st);
     if (e != hipSuccess) return e;
     if (copy) p.w = to, p.w_stride = l.Kp;
     const int b = kind == kTile256 ? 256 : kind == kRing128 ? 128 : 64;
@@ -614,14 +617,14 @@ template <typename T> hipError_t launch1(const LinearArgs &a, const CodesLayout 
 
 }  // namespace
 
-int64_t linear_workspace(int64_t M, int64_t N, int64_t K) {
+int64_t linear_workspace(int64_t M, int64_t N, int64_t K, bool rows) {
     const CodesLayout l = codes_layout(nullptr, M, K);
     const int64_t splits = splits_of(M, N, K);
-    return l.bytes + (needs_copy(M, N, K) ? N * l.Kp : 0) + (splits > 1 ? tiles(M, N, 64) * (splits * 16384 + 4) : 0);
+    return (rows ? 0 : l.bytes) + (needs_copy(M, N, K) ? N * l.Kp : 0) + (splits > 1 ? tiles(M, N, 64) * (splits * 16384 + 4) : 0);
 }
 
 hipError_t launch_int8_linear(const LinearArgs &a, hipStream_t st) {
-    const CodesLayout l = codes_layout(a.workspace, a.M, a.K);
+    const CodesLayout l = codes_layout(a.rows ? const_cast<void *>(a.rows) : a.workspace, a.M, a.K);
     switch (a.dtype) {
         case CBS_DTYPE_F32: return launch1<float>(a, l, st);
         case CBS_DTYPE_BF16: return launch1<__bf16>(a, l, st);

@@ -128,6 +128,24 @@ hipError_t launch1(const LinearArgs &a, const CodesLayout &l, int8_t *to, int *z
 
 }  // namespace
 
+hipError_t launch_beside_rows(const LinearArgs &a, const CodesLayout &l, int8_t *to, int *zeros, int count, hipStream_t st) {
+    const int64_t pieces = to ? (int64_t)a.N * (l.Kp / 16) : 0;
+    int64_t piece = 0;
+    do {
+        const int copies = (int)std::min<int64_t>(kMostRows, (pieces - piece + kThreads - 1) / kThreads);
+        // with nothing to copy, N = 0 leaves the one workgroup with the zeros
+        const Beside beside{0, a.w, to, to ? a.N : 0, piece, zeros, zeros && piece == 0 ? count : 0};
+        quant_rows<float, 64><<<(unsigned)std::max(1, copies), kThreads, 0, st>>>(nullptr, 0, 0, a.K, l.Kp, l.rows, nullptr,
+                                                                                  nullptr, beside);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        piece += (int64_t)copies * kThreads;
+    } while (piece < pieces);
+    return hipSuccess;
+}
+
+int64_t rows8_bytes(int64_t M, int64_t K) { return codes_layout(nullptr, M, K).bytes; }
+
 CodesLayout codes_layout(void *workspace, int64_t M, int64_t K) {
     CodesLayout l;
     l.rows = (int)((M + 15) / 16 * 16);

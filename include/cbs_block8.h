@@ -52,6 +52,21 @@ int cbs_int8_linear(conv_bn_silu_t handle, const void *x, int64_t x_stride, cons
 /* Bytes of workspace of that call; -1 for sizes it refuses. */
 int64_t cbs_int8_linear_workspace(int64_t M, int64_t N, int64_t K);
 
+/* Rows in 8 bits, as cbs_add_rms_norm (cbs_step.h) gives them and the layer below takes them, [M][K]: one
+ * buffer of cbs_rows8_bytes(M, K) bytes (-1 for sizes that the layer refuses), aligned to 16:
+ *   fp32 scales [R], R = M up to a whole 16;
+ *   codes in blocks of 64 along K, [ceil(K / 128) * 2][R][64]: code (m, k) at ((k / 64) * R + m) * 64 + k % 64,
+ *   zeros from K on.  What belongs to rows past M may hold anything.
+ * So the matrix kernels find the fragments of neighbouring rows side by side. */
+int64_t cbs_rows8_bytes(int64_t M, int64_t K);
+
+/* cbs_int8_linear of such rows: the same result as from the x that they were made of.  dtype is
+ * that of y.  The workspace is smaller: cbs_int8_linear_rows_workspace(M, N, K), often 0. */
+int cbs_int8_linear_rows(conv_bn_silu_t handle, const void *rows, const int8_t *w, const float *w_scale,
+                         const float *bias, void *y, int64_t M, int64_t N, int64_t K, int dtype, int activation,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+int64_t cbs_int8_linear_rows_workspace(int64_t M, int64_t N, int64_t K);
+
 /* A paged cache.  k, v: contiguous [pages][heads][page_size][dim] of dtype (I8,
  * F32, BF16 or F16); k_scale, v_scale: contiguous fp32 [pages][heads][page_size]
  * for I8, NULL otherwise.  A token's slot is page * page_size + offset.
