@@ -1,140 +1,184 @@
 // k_norm.hip -- the residual's addition with the root-mean-square norm:
 // h = x + residual, y = h w / sqrt(mean(h^2) + eps), y in x's type or as rows in 8 bits.
 //
-// Bound by HBM: x and the residual are read once, h and y written once.  A row belongs to a
-// team of lanes and stays in their registers, 32 values a lane, from the sum of its squares to
-// y; longer rows read h a second time.
+// Bound by HBM: x and the residual are read once, h and y written once, and a row stays in
+// registers in between.  8 values a lane, and as many lanes as the row has 8s: many short workgroups, each with
+// one access of a tensor a lane on its way, draw the most (16384 x 8192, bf16 with residual: 256 lanes with 32
+// values each 203 us, 512 with 16 207, 1024 with 8 180; 1.07 GB at the rate of a large copy, 6.3 TB/s: 170).
+// Rows beyond 8192 take 16 values a lane, those beyond 16384 read h a second time.  What the memory-side cache cannot
+// hold passes by the caches (180 -> 170 us; outputs in 8 bits stay, for the layer reads them: 8192 x 8192 with
+// what is read passing by as well 220 us into a layer of 1024, without 214), and eight workgroups of neighbouring rows
+// share an XCD (172 -> 169).  Together 168 us, 6.4 TB/s.
+//   Rows of 1024 (131072 of them) 172 us for 170, of 256 (300000) 99 for 98, of 128 (a million, no residual) 90
+//   for 85; 16384 wide 173 for 170; 32768 wide 206 for 170; one row of 4096: 2.8 us on the GPU, 6 a call.
 //
-// Squares are summed in 64 bits: no row of finite numbers overflows or vanishes on the way, and
-// the matter is hidden under the loads (a CU has some 200 cycles for 64 values there).  r = 1 /
-// sqrt(...) and h r are in 64 bits too: where h is large, r lies below fp32's normal numbers.
+// Squares are summed in 64 bits: no row of finite numbers overflows or vanishes on the way.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 
 #include "b8_device.h"
 #include "b8_linear.h"
+#include "st_device.h"
 #include "st_launch.h"
 
 namespace cbs {
 namespace {
 
-constexpr int kChunks = 4;  // of 8 values a lane keeps
-
-// 8 values from k on, zeros from K on.
-template <typename T> __device__ __forceinline__ f32x8 load_chunk(const T *row, int k, int K) {
-    f32x8 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (k + 8 <= K) return Value<T>::load8(row + k);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (k + i < K) x[i] = Value<T>::load1(row + k + i);
-    return x;
-}
-template <typename T> __device__ __forceinline__ void store_chunk(T *row, int k, int K, f32x8 v) {
-    if (k + 8 <= K) {
-        Value<T>::store8(row + k, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (k + i < K) Value<T>::store1(row + k + i, v[i]);
-}
-
 struct NormParams {
     NormArgs a;
     CodesLayout l;  // of y in 8 bits
     int m0;         // row that the launch begins with
+    double inv_k;   // 1 / K
 };
 
-// T: type of x and y, R: of the residual and the sum.  TEAM lanes to a row, 64 or more of them a
-// workgroup of their own waves.
-template <typename T, typename R, int TEAM, bool INT8>
-__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void add_rms_norm(const NormParams p) {
-    constexpr int kThreads = TEAM < 256 ? 256 : TEAM, kWaves = TEAM / 64;
-    __shared__ double squares_of[kWaves > 0 ? kWaves : 1];
-    __shared__ uint32_t top_of[kWaves > 0 ? kWaves : 1];
+// 1 / sqrt(s) for s > 0: the instruction is good to 2^-23, one step of Newton's doubles the bits.
+__device__ __forceinline__ double reciprocal_root(double s) {
+    const double r = __builtin_amdgcn_rsq(s), better = __builtin_fma(0.5 * r, __builtin_fma(-s * r, r, 1.0), r);
+    return s == INFINITY ? 0.0 : better;
+}
+
+// 8 weights on their way: they are asked for before the sum of squares, and wanted after it.  Wide ones beside
+// narrow values are not, for the registers they take would cost more than the wait.
+template <typename T> struct Weights {
+    u32x4 raw[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const NormArgs &a, int k) {
+        if (k + 8 > a.K || !a.weight || a.weight_dtype != a.dtype) return;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) raw[i] = ((const Any16 *)((const T *)a.weight + k))[i].v;
+    }
+    __device__ __forceinline__ f32x8 get(const NormArgs &a, int k) const {
+        if (!a.weight) return f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+        if (a.weight_dtype != a.dtype) return load_chunk<false>((const float *)a.weight, k, a.K);
+        return k + 8 > a.K ? load_chunk<false>((const T *)a.weight, k, a.K) : Held<T>{raw}.get();
+    }
+};
+
+// T: type of x and y, R: of the residual and the sum.  TEAM lanes to a row; teams of 128 and less share a
+// workgroup of 256, or a row has a workgroup (TEAM 0).  CHUNKS: of 8 values a lane keeps.  STREAM: the tensors pass by
+// the caches.
+template <typename T, typename R, int TEAM, int CHUNKS, bool INT8, bool STREAM>
+__global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormParams p) {
+    constexpr int kLanes = TEAM == 0 || TEAM > 64 ? 64 : TEAM, kMostWaves = TEAM ? 4 : 16;
+    constexpr bool kMeet = TEAM == 0 || TEAM > 64;  // a row's waves meet in LDS
+    constexpr bool kOnce = STREAM && !INT8;
+    __shared__ double squares_of[kMostWaves];
+    __shared__ uint32_t top_of[kMostWaves];
     const NormArgs &a = p.a;
-    const int lane = (int)threadIdx.x % TEAM, K = a.K;
-    const int m = p.m0 + (int)blockIdx.x * (kThreads / TEAM) + (int)threadIdx.x / TEAM;
-    if (TEAM < 256 && m >= a.M) return;  // larger teams have a workgroup to themselves
+    const int team = TEAM ? TEAM : (int)blockDim.x, tid = (int)threadIdx.x, lane = tid % team, K = a.K;
+    // workgroups go to the eight XCDs in turn; of 64, each gets 8 with rows side by side
+    const int id = (int)blockIdx.x, group = id & ~63, in = id & 63;
+    const int place = group + 64 <= (int)gridDim.x ? group + in % 8 * 8 + in / 8 : id;
+    int m = p.m0 + (TEAM ? place * (256 / team) + tid / team : place);
+    const bool mine = m < a.M;
+    if (!kMeet && !mine) return;
+    m = min(m, a.M - 1);  // reads the last row and writes nothing
     const T *const x = (const T *)a.x + (int64_t)m * a.x_stride;
     const R *const residual = a.residual ? (const R *)a.residual + (int64_t)m * a.residual_stride : nullptr;
     R *const sum = (R *)a.sum + (int64_t)m * a.sum_stride;
+    const int end = mine ? K : 0, code_end = mine ? p.l.Kp : 0;  // of what is written
 
-    auto take = [&](int k) {
-        f32x8 h = load_chunk<T>(x, k, K);
-        if (residual) {
-            h += load_chunk<R>(residual, k, K);
+    auto add = [&](f32x8 h, f32x8 r, int k) {
+        h += r;
+        const Held<R> v(h);
+        if (k < end) v.template store<STREAM>(sum, k, K);
+        return v;
+    };
+    auto again = [&](int k) { return residual ? load_chunk<false>(sum, k, K) : load_chunk<false>(x, k, K); };
+    auto square = [&](double &to, f32x8 h) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = (float)(R)h[i];
-            store_chunk<R>(sum, k, K, h);
+        for (int i = 0; i < 8; ++i) to = __builtin_fma((double)h[i], (double)h[i], to);
+    };
+    const int span = CHUNKS * team * 8;
+    // h is a number of R's with a residual, of T's without, which R holds too
+    Held<R> keep[CHUNKS];
+    Weights<T> weights[CHUNKS];
+    {
+        f32x8 h[CHUNKS];
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) h[c] = load_chunk<kOnce>(x, (c * team + lane) * 8, K);
+        if (residual) {
+            f32x8 r[CHUNKS];
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) r[c] = load_chunk<kOnce>(residual, (c * team + lane) * 8, K);
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) weights[c].load(a, (c * team + lane) * 8);
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) keep[c] = add(h[c], r[c], (c * team + lane) * 8);
+        } else {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) weights[c].load(a, (c * team + lane) * 8);
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) keep[c] = Held<R>(h[c]);
+        }
+    }
+    double part[CHUNKS] = {}, squares = 0;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) square(part[c], keep[c].get());
+    for (int k = span + lane * 8; k < K; k += team * 8) {
+        const f32x8 h = load_chunk<false>(x, k, K);
+        square(squares, residual ? add(h, load_chunk<false>(residual, k, K), k).get() : h);
+    }
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) squares += part[c];
+    squares = team_sum<kLanes>(squares);
+    // a row's waves, and this lane's of them where they meet
+    const int waves = team / 64, wave0 = TEAM == 128 ? tid / 128 * 2 : 0, its = wave0 + tid % (TEAM ? 2 : 16);
+    const bool there = its < wave0 + waves;
+    if constexpr (kMeet) {
+        if (tid % 64 == 0) squares_of[tid / 64] = squares;
+        __syncthreads();
+        squares = team_sum<TEAM ? 2 : 16>(there ? squares_of[its] : 0.0);
+    }
+    // h r in fp32 with one rounding: r in two parts, and where it comes near fp32's smallest numbers h and r
+    // meet half way
+    double r = reciprocal_root(__builtin_fma(squares, p.inv_k, (double)a.eps));
+    const float fit = r < 0x1p-64 ? 0x1p-64f : 1.f;
+    if (r < 0x1p-64) r *= 0x1p64;
+    const float r_hi = (float)r, r_lo = (float)(r - (double)r_hi);
+    auto scaled = [&](f32x8 h, f32x8 w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v = h[i] * fit;
+            h[i] = __builtin_fmaf(v, r_hi, v * r_lo) * w[i];
         }
         return h;
     };
-    auto again = [&](int k) { return residual ? load_chunk<R>(sum, k, K) : load_chunk<T>(x, k, K); };
-    double squares = 0;
-    auto square = [&](f32x8 h) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) squares = __builtin_fma((double)h[i], (double)h[i], squares);
-    };
-    constexpr int kSpan = kChunks * TEAM * 8;
-    f32x8 keep[kChunks];
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        keep[c] = take((c * TEAM + lane) * 8);
-        square(keep[c]);
-    }
-    for (int k = kSpan + lane * 8; k < K; k += TEAM * 8) square(take(k));
-#pragma unroll
-    for (int o = 1; o < (TEAM < 64 ? TEAM : 64); o *= 2) squares += __shfl_xor(squares, o, 64);
-    if constexpr (TEAM > 64) {
-        if (lane % 64 == 0) squares_of[lane / 64] = squares;
-        __syncthreads();
-        squares = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) squares += squares_of[w];
-    }
-    const double r = 1.0 / __builtin_sqrt(squares / K + (double)a.eps);
-
-    auto scaled = [&](f32x8 h, int k) {
-        f32x8 w = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-        if (a.weight)
-            w = a.weight_dtype == CBS_DTYPE_F32 ? load_chunk<float>((const float *)a.weight, k, K)
-                                                : load_chunk<T>((const T *)a.weight, k, K);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = (float)((double)h[i] * r) * w[i];
-        return h;
+    auto scaled_again = [&](int k) {
+        Weights<T> w;
+        w.load(a, k);
+        return scaled(again(k), w.get(a, k));
     };
     if constexpr (!INT8) {
         T *const y = (T *)a.y + (int64_t)m * K;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int k = (c * TEAM + lane) * 8;
-            if (k < K) store_chunk<T>(y, k, K, scaled(keep[c], k));
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int k = (c * team + lane) * 8;
+            if (k < end) Held<T>(scaled(keep[c].get(), weights[c].get(a, k))).template store<STREAM>(y, k, K);
         }
-        for (int k = kSpan + lane * 8; k < K; k += TEAM * 8) store_chunk<T>(y, k, K, scaled(again(k), k));
+        for (int k = span + lane * 8; k < end; k += team * 8) Held<T>(scaled_again(k)).template store<STREAM>(y, k, K);
     } else {
         uint32_t top = 0;
         auto largest = [&](f32x8 y) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = max(top, magnitude(y[i]));
         };
+        // two chunks are scaled twice: kept, they would cost the registers of a second workgroup on the CU
+        f32x8 y = {};
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int k = (c * TEAM + lane) * 8;
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int k = (c * team + lane) * 8;
             if (k < K) {
-                keep[c] = scaled(keep[c], k);
-                largest(keep[c]);
+                y = scaled(keep[c].get(), weights[c].get(a, k));
+                largest(y);
             }
         }
-        for (int k = kSpan + lane * 8; k < K; k += TEAM * 8) largest(scaled(again(k), k));
-#pragma unroll
-        for (int o = 1; o < (TEAM < 64 ? TEAM : 64); o *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
-        if constexpr (TEAM > 64) {
-            if (lane % 64 == 0) top_of[lane / 64] = top;
+        for (int k = span + lane * 8; k < end; k += team * 8) largest(scaled_again(k));
+        top = team_max_of<kLanes>(top);
+        if constexpr (kMeet) {
+            if (tid % 64 == 0) top_of[tid / 64] = top;
             __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) top = max(top, top_of[w]);
+            top = team_max_of<TEAM ? 2 : 16>(there ? top_of[its] : 0u);
         }
         const float s = row_scale(top), inv = row_inverse(s, top);
         auto codes = [&](f32x8 y, int k) {
@@ -144,33 +188,42 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void add_rms_norm(const No
                 u32x2{pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])};
         };
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int k = (c * TEAM + lane) * 8;
-            if (k < p.l.Kp) codes(keep[c], k);
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int k = (c * team + lane) * 8;
+            if (CHUNKS > 1) y = k < K ? scaled(keep[c].get(), weights[c].get(a, k)) : f32x8{};
+            if (k < code_end) codes(y, k);
         }
-        for (int k = kSpan + lane * 8; k < p.l.Kp; k += TEAM * 8)
-            codes(k < K ? scaled(again(k), k) : f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, k);
-        if (lane == 0) p.l.scales[m] = s;
+        for (int k = span + lane * 8; k < code_end; k += team * 8)
+            codes(k < K ? scaled_again(k) : f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, k);
+        if (lane == 0 && mine) p.l.scales[m] = s;
     }
 }
 
-template <typename T, typename R, int TEAM, bool INT8> hipError_t launch4(const NormArgs &a, const CodesLayout &l, hipStream_t st) {
-    constexpr int kThreads = TEAM < 256 ? 256 : TEAM, kRows = kThreads / TEAM;
+template <typename T, typename R, int TEAM, int CHUNKS, bool INT8, bool STREAM>
+hipError_t launch5(const NormArgs &a, const CodesLayout &l, hipStream_t st) {
+    const int rows = TEAM ? 256 / TEAM : 1, threads = TEAM ? 256 : std::min(1024, (a.K + 512 * CHUNKS - 1) / (512 * CHUNKS) * 64);
     // one launch but for the largest sizes: a launch holds fewer than 2^32 threads
     constexpr int kMost = 1 << 21;
     hipError_t e = hipSuccess;
     for (int m0 = 0; m0 < a.M && e == hipSuccess; m0 += kMost) {
-        const NormParams p{a, l, m0};
-        add_rms_norm<T, R, TEAM, INT8><<<(unsigned)((std::min(kMost, a.M - m0) + kRows - 1) / kRows), kThreads, 0, st>>>(p);
+        const NormParams p{a, l, m0, 1.0 / a.K};
+        const unsigned grid = (unsigned)((std::min(kMost, a.M - m0) + rows - 1) / rows);
+        add_rms_norm<T, R, TEAM, CHUNKS, INT8, STREAM><<<grid, threads, 0, st>>>(p);
         e = hipGetLastError();
     }
     return e;
 }
+template <typename T, typename R, int TEAM, int CHUNKS, bool INT8> hipError_t launch4(const NormArgs &a, const CodesLayout &l, hipStream_t st) {
+    const int64_t bytes = (int64_t)a.M * a.K * ((a.int8 ? 1 : 2) * sizeof(T) + (a.residual ? 2 * sizeof(R) : 0));
+    return bytes > kCached ? launch5<T, R, TEAM, CHUNKS, INT8, true>(a, l, st) : launch5<T, R, TEAM, CHUNKS, INT8, false>(a, l, st);
+}
 template <typename T, typename R, bool INT8> hipError_t launch3(const NormArgs &a, const CodesLayout &l, hipStream_t st) {
-    if (a.K <= 512) return launch4<T, R, 16, INT8>(a, l, st);
-    if (a.K <= 2048) return launch4<T, R, 64, INT8>(a, l, st);
-    if (a.K <= 8192) return launch4<T, R, 256, INT8>(a, l, st);
-    return launch4<T, R, 512, INT8>(a, l, st);
+    if (a.K <= 128) return launch4<T, R, 16, 1, INT8>(a, l, st);
+    if (a.K <= 256) return launch4<T, R, 32, 1, INT8>(a, l, st);
+    if (a.K <= 512) return launch4<T, R, 64, 1, INT8>(a, l, st);
+    if (a.K <= 1024) return launch4<T, R, 128, 1, INT8>(a, l, st);
+    if (a.K <= 8192) return launch4<T, R, 0, 1, INT8>(a, l, st);
+    return launch4<T, R, 0, 2, INT8>(a, l, st);
 }
 template <typename T, typename R> hipError_t launch2(const NormArgs &a, hipStream_t st) {
     if (a.int8) return launch3<T, R, true>(a, codes_layout(a.y, a.M, a.K), st);
