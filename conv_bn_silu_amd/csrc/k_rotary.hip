@@ -3,31 +3,38 @@
 //
 // Angles.  position * frequency / 2 pi in turns, in 64 bits (fp32 would be off by 2^-25 of the
 // position: 0.04 radians at a million); less the nearest quarter it fits fp32, where the series
-// of sine and cosine on an eighth of a turn either way end below half a step.  A workgroup has a few tokens,
-// works their angles out once, into LDS, and turns all their heads by them.
+// of sine and cosine on an eighth of a turn either way end below half a step.  A workgroup works its tokens'
+// angles out once, into LDS, while its first rows are on their way.
 //
-// Bound by HBM: every row is read once and written once.
+// Bound by HBM: every row is read once and written once.  32768 tokens, 32 heads over 8, dim 128, bf16 into
+// 8 bits: 134 us, 5.5 TB/s (740 MB; a large copy: 6.3 TB/s, 117 us).  Queries, keys and values go to different
+// workgroups, whose addresses and branches are then the same for all lanes (a workgroup with all rows of
+// a token, each lane looking up its own: 185 us, 250 vector instructions a row of 16 lanes' values); a team takes two rows at
+// most, one after the other (eight: 146).  Other forms, us and what a copy would take: into 16 bits 145, 128;
+// fp32 into 8 bits 263, 224; dim 64 138, 101; 8 heads over 8 70, 53; 8192 tokens of 40 heads without
+// a cache 31, 27; 5001 ragged ones 9, 6; one or 64 tokens 3 on the GPU, 8 a call.  Pairs that are no whole 8
+// make smaller pieces: dim 80 with 20 pairs 140, 60; dim 100 with 50 118, 67 (any numbers, through LDS: 195 and 238).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <type_traits>
 
 #include "b8_device.h"
+#include "st_device.h"
 #include "st_launch.h"
 
 namespace cbs {
 namespace {
 
-constexpr int kMostDim = 512, kMostPairs = kMostDim / 2;
-constexpr int kMostThreads = 1024;
 
 struct RotaryParams {
     RotaryArgs a;
-    FastDiv rows;     // of a token: its queries, keys and values
     FastDiv page;
     uint32_t slots;   // pages * page size
     int64_t token, end;  // tokens of the launch
-    int tokens;          // to a workgroup
+    // rotary_pieces: workgroups of the queries and of the keys (and of the values), tokens of each
+    int q_blocks, kv_blocks, q_tokens, kv_tokens;
+    FastDiv q_heads, kv_heads, pairs;
 };
 
 // (cos, sin) of position * frequency, times the magnitude.
@@ -50,207 +57,347 @@ __device__ __forceinline__ void turn(float &a, float &b, float2 by) {
     b = b * by.x + x * by.y;
 }
 
-// A row of a token: its tensor, and where it goes.
-template <typename T> struct Row {
-    const T *from;
-    T *to;               // queries
-    int side;            // 0 queries, 1 keys, 2 values
-    int64_t at;          // keys and values: their row of the cache, -1 for nowhere
-    __device__ __forceinline__ Row(const RotaryParams &p, int64_t token, int row) {
-        const RotaryArgs &a = p.a;
-        side = row < a.heads ? 0 : row < a.heads + a.kv_heads ? 1 : 2;
-        to = nullptr, at = -1;
-        if (side == 0) {
-            from = (const T *)a.q + token * a.q_token + row * a.q_head;
-            to = (T *)a.q_out + token * a.out_token + row * a.out_head;
-            return;
+__device__ __forceinline__ int64_t cache_line(const RotaryParams &p, uint32_t slot, int head) {
+    const uint32_t page = p.page.div(slot);
+    return ((int64_t)page * p.a.cache.heads + head) * p.page.d + (slot - page * p.page.d);
+}
+
+constexpr int kMostThreads = 512;
+
+// P values as T holds them, at any address.
+template <typename T, int P> struct Piece {
+    static constexpr int kWords = P * (int)sizeof(T) / 4, kParts = kWords > 4 ? kWords / 4 : 1;
+    typedef uint32_t words __attribute__((ext_vector_type(kWords / kParts)));
+    typedef T values __attribute__((ext_vector_type(P)));
+    typedef float floats __attribute__((ext_vector_type(P)));
+    typedef words __attribute__((aligned(1))) any;
+    struct Raw {
+        words w[kParts];
+    } raw;
+    Piece() = default;
+    __device__ __forceinline__ explicit Piece(const float *x) {
+        floats v;
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[e] = x[e];
+        raw = __builtin_bit_cast(Raw, __builtin_convertvector(v, values));
+    }
+    template <bool STREAM> __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) raw.w[i] = STREAM ? __builtin_nontemporal_load((const any *)p + i) : ((const any *)p)[i];
+    }
+    template <bool STREAM> __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            if constexpr (STREAM) __builtin_nontemporal_store(raw.w[i], (any *)p + i);
+            else ((any *)p)[i] = raw.w[i];
         }
-        const int head = row - a.heads - (side == 2 ? a.kv_heads : 0);
-        from = side == 1 ? (const T *)a.k + token * a.k_token + head * a.k_head : (const T *)a.v + token * a.v_token + head * a.v_head;
-        const uint32_t slot = (uint32_t)a.slots[token];
-        if (slot < p.slots) {  // negative slots are large numbers here
-            const uint32_t page = p.page.div(slot);
-            at = ((int64_t)page * a.cache.heads + head) * p.page.d + (slot - page * p.page.d);
-        }
+    }
+    __device__ __forceinline__ void get(float *x) const {
+        const floats v = __builtin_convertvector(__builtin_bit_cast(values, raw), floats);
+#pragma unroll
+        for (int e = 0; e < P; ++e) x[e] = v[e];
     }
 };
 
-// A workgroup's angles, by all of its threads.
-__device__ __forceinline__ void fill_turns(const RotaryParams &p, float2 *turns, int64_t token0, int tokens) {
-    const int pairs = p.a.rotary.pairs;
-    for (int i = (int)threadIdx.x; i < tokens * pairs; i += (int)blockDim.x) {
-        const int t = i / pairs;
-        turns[i] = turn_of(p.a.rotary, p.a.positions[token0 + t], i - t * pairs);
-    }
-    __syncthreads();
-}
+// Where the angle of pair i of a token lies in LDS: lanes read P of them, two at a time, and so side by side.
+template <int P> __device__ __forceinline__ int turn_at(int i, int pairs) { return i % P / 2 * (pairs / P * 2) + i / P * 2 + i % 2; }
 
-// Where dims and pairs come in whole 8s: a row belongs to a team of LANES lanes, two pieces of 8 a lane,
-// of which a lane of the turned part has both halves of its pairs.  C: the cache's type (without a cache,
-// T).
-template <typename T, typename C, int LANES, bool INTERLEAVED>
-__global__ __launch_bounds__(kMostThreads) void rotary_pieces(const RotaryParams p) {
-    extern __shared__ float2 turns[];
+// Where dims and pairs come in whole Ps (8, 4 or 2): a row belongs to a team of LANES lanes, two pieces of P a
+// lane, of which a lane of the turned part has both halves of its pairs.  A workgroup has the queries, the keys or
+// the values (SIDE) of some tokens, and while a team turns one row the next one is on its way.  C: the
+// cache's type (without a cache, T).  STREAM: the tensors pass by the caches.
+template <typename T, typename C, int P, int LANES, bool INTERLEAVED, bool STREAM, int SIDE>
+__device__ __forceinline__ void rotary_side(const RotaryParams &p, int block, float2 *turns) {
     const RotaryArgs &a = p.a;
-    const int64_t token0 = p.token + (int64_t)blockIdx.x * p.tokens;
-    const int tokens = (int)min((int64_t)p.tokens, p.end - token0);
-    fill_turns(p, turns, token0, tokens);
+    const int teams = (int)blockDim.x / LANES;
+    const int each = SIDE == 0 ? p.q_tokens : p.kv_tokens, heads = SIDE == 0 ? a.heads : a.kv_heads;
+    const int64_t token0 = p.token + (int64_t)block * each;
+    const int tokens = (int)min((int64_t)each, p.end - token0), tasks = tokens * heads;
+    const FastDiv &by_heads = SIDE == 0 ? p.q_heads : p.kv_heads;
+    const int64_t token_step = SIDE == 0 ? a.q_token : SIDE == 1 ? a.k_token : a.v_token;
+    const int64_t head_step = SIDE == 0 ? a.q_head : SIDE == 1 ? a.k_head : a.v_head;
+    const T *const from = (const T *)(SIDE == 0 ? a.q : SIDE == 1 ? a.k : a.v) + token0 * token_step;
 
-    const int lane = (int)threadIdx.x % LANES, pairs = a.rotary.pairs, half = pairs / 8;
+    const int lane = (int)threadIdx.x % LANES, pairs = a.rotary.pairs, half = pairs / P, team = (int)threadIdx.x / LANES;
     // the lane's pieces, and whether they are turned; past dim there is nothing
-    const bool turned = INTERLEAVED ? 16 * lane < 2 * pairs : lane < half;
-    const int d0 = INTERLEAVED || lane >= half ? 16 * lane : 8 * lane, d1 = INTERLEAVED || lane >= half ? d0 + 8 : d0 + pairs;
+    const bool turned = INTERLEAVED ? P * lane < pairs : lane < half;
+    const bool apart = !INTERLEAVED && lane < half;  // the second is not the one after the first
+    const int d0 = apart ? P * lane : 2 * P * lane, d1 = apart ? d0 + pairs : d0 + P;
     const bool has0 = d0 < a.dim, has1 = d1 < a.dim;
-    const int team = (int)threadIdx.x / LANES, teams = (int)blockDim.x / LANES;
-    for (int i = team; i < tokens * (int)p.rows.d; i += teams) {
-        const int t = (int)p.rows.div((uint32_t)i);
-        const Row<T> row(p, token0 + t, i - t * (int)p.rows.d);
-        if (row.side != 0 && row.at < 0) continue;
-        f32x8 x[2] = {};
-        if (has0) x[0] = Value<T>::load8(row.from + d0);
-        if (has1) x[1] = Value<T>::load8(row.from + d1);
-        if (turned && row.side != 2) {
-            const float2 *by = turns + t * pairs;
-            if constexpr (INTERLEAVED) {
+
+    Piece<T, P> next[2] = {};
+    uint32_t next_slot = 0;
+    auto take = [&](int i) {
+        const int t = (int)by_heads.div((uint32_t)i), h = i - t * heads;
+        const T *const row = from + t * token_step + h * head_step;
+        if (has0) next[0].template load<STREAM>(row + d0);
+        if (has1) next[1].template load<STREAM>(row + d1);
+        if constexpr (SIDE != 0) next_slot = (uint32_t)a.slots[token0 + t];
+    };
+    if (team < tasks) take(team);
+    if constexpr (SIDE != 2) {
+        for (int i = (int)threadIdx.x; i < tokens * pairs; i += (int)blockDim.x) {
+            const int t = (int)p.pairs.div((uint32_t)i), pair = i - t * pairs;
+            turns[t * pairs + (INTERLEAVED ? pair : turn_at<P>(pair, pairs))] = turn_of(a.rotary, a.positions[token0 + t], pair);
+        }
+        __syncthreads();
+    }
+    for (int i = team; i < tasks; i += teams) {
+        float x[2 * P];
+        next[0].get(x), next[1].get(x + P);
+        const uint32_t slot = next_slot;
+        if (i + teams < tasks) take(i + teams);
+        const int t = (int)by_heads.div((uint32_t)i), h = i - t * heads;
+        if (SIDE != 2 && turned) {
+            const float2 *const by = turns + t * pairs;
 #pragma unroll
-                for (int side = 0; side < 2; ++side)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int pair = 8 * lane + 4 * side + e;
-                        if (pair < pairs) {
-                            float u = x[side][2 * e], v = x[side][2 * e + 1];
-                            turn(u, v, by[pair]);
-                            x[side][2 * e] = u, x[side][2 * e + 1] = v;
-                        }
-                    }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float u = x[0][e], v = x[1][e];
-                    turn(u, v, by[8 * lane + e]);
-                    x[0][e] = u, x[1][e] = v;
+            for (int e = 0; e < P; ++e) {
+                if constexpr (INTERLEAVED) {
+                    if (P * lane + e < pairs) turn(x[2 * e], x[2 * e + 1], by[P * lane + e]);
+                } else {
+                    turn(x[e], x[P + e], by[turn_at<P>(P * lane + e, pairs)]);
                 }
             }
         }
-        if (row.side == 0) {
-            if (has0) Value<T>::store8(row.to + d0, x[0]);
-            if (has1) Value<T>::store8(row.to + d1, x[1]);
-            continue;
-        }
-        C *const to = (C *)(row.side == 1 ? a.cache.k : a.cache.v) + row.at * a.dim;
-        if constexpr (std::is_same_v<C, int8_t>) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = max(top, max(magnitude(x[0][e]), magnitude(x[1][e])));
-#pragma unroll
-            for (int o = 1; o < LANES; o *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o, LANES));
-            const float s = row_scale(top), inv = row_inverse(s, top);
-#pragma unroll
-            for (int side = 0; side < 2; ++side) {
-                int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (inv != 0.f) row_codes8(x[side], s, inv, c);
-                if (side ? has1 : has0)
-                    *(u32x2 *)(to + (side ? d1 : d0)) = u32x2{pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])};
-            }
-            if (lane == 0) (row.side == 1 ? a.cache.k_scale : a.cache.v_scale)[row.at] = s;
+        if constexpr (SIDE == 0) {
+            T *const to = (T *)a.q_out + token0 * a.out_token + t * a.out_token + h * a.out_head;
+            if (has0) Piece<T, P>(x).template store<STREAM>(to + d0);
+            if (has1) Piece<T, P>(x + P).template store<STREAM>(to + d1);
         } else {
-            if (has0) Value<C>::store8(to + d0, x[0]);
-            if (has1) Value<C>::store8(to + d1, x[1]);
+            if (slot >= p.slots) continue;  // negative slots are large numbers here
+            const int64_t line = cache_line(p, slot, h);
+            C *const to = (C *)(SIDE == 1 ? a.cache.k : a.cache.v) + line * a.dim;
+            if constexpr (std::is_same_v<C, int8_t>) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < 2 * P; ++e) top = max(top, magnitude(x[e]));
+                top = team_max_of<LANES>(top);
+                const float s = row_scale(top), inv = row_inverse(s, top);
+                int c[16] = {};
+                if (inv != 0.f) {
+#pragma unroll
+                    for (int g = 0; g < (2 * P + 7) / 8; ++g) {
+                        f32x8 v = {};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (8 * g + e < 2 * P) v[e] = x[8 * g + e];
+                        int eight[8];
+                        row_codes8(v, s, inv, eight);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) c[8 * g + e] = eight[e];
+                    }
+                }
+                if constexpr (P == 8) {
+                    const u32x2 codes[2] = {{pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])},
+                                            {pack_codes(c[8], c[9], c[10], c[11]), pack_codes(c[12], c[13], c[14], c[15])}};
+                    // pieces that lie apart: two lanes exchange one each, for stores of 16 bytes
+                    const bool odd = lane & 1, trade = !INTERLEAVED && lane < (half & ~1);
+                    const u32x2 give = odd ? codes[0] : codes[1];
+                    const u32x2 got = {lane_from<kSwap1>(give.x, give.x), lane_from<kSwap1>(give.y, give.y)};
+                    if (trade || (!apart && has1)) {
+                        const u32x2 lo = trade && odd ? got : codes[0], hi = trade && !odd ? got : codes[1];
+                        ((Any16 *)(to + (trade && odd ? d1 - 8 : d0)))->v = u32x4{lo.x, lo.y, hi.x, hi.y};
+                    } else {
+                        if (has0) *(u32x2 *)(to + d0) = codes[0];
+                        if (has1) *(u32x2 *)(to + d1) = codes[1];
+                    }
+                } else {
+                    const uint32_t lo = pack_codes(c[0], c[1], c[2], c[3]), hi = pack_codes(c[4], c[5], c[6], c[7]);
+                    if constexpr (P == 4) {
+                        if (has0) *(uint32_t *)(to + d0) = lo;
+                        if (has1) *(uint32_t *)(to + d1) = hi;
+                    } else {
+                        if (has0) *(uint16_t *)(to + d0) = (uint16_t)lo;
+                        if (has1) *(uint16_t *)(to + d1) = (uint16_t)(lo >> 16);
+                    }
+                }
+                if (lane == 0) (SIDE == 1 ? a.cache.k_scale : a.cache.v_scale)[line] = s;
+            } else {
+                if (has0) Piece<C, P>(x).template store<false>(to + d0);
+                if (has1) Piece<C, P>(x + P).template store<false>(to + d1);
+            }
         }
     }
 }
 
-// Any dims and pairs: a wave to a row, every 64th value a lane.  A row goes through LDS, where each
-// value finds its partner.  All of a row is read before any of it is written, which may be in its place.
-template <typename T, typename C>
-__global__ __launch_bounds__(256) void rotary_values(const RotaryParams p) {
-    constexpr int kEach = kMostDim / 64;
-    __shared__ float2 turns[kMostPairs];
-    __shared__ float rows[4][kMostDim];
+template <typename T, typename C, int P, int LANES, bool INTERLEAVED, bool STREAM>
+__global__ __launch_bounds__(kMostThreads) void rotary_pieces(const RotaryParams p) {
+    extern __shared__ __attribute__((aligned(16))) float2 turns[];
+    const int block = (int)blockIdx.x;
+    if (block < p.q_blocks) rotary_side<T, C, P, LANES, INTERLEAVED, STREAM, 0>(p, block, turns);
+    else if (block < p.q_blocks + p.kv_blocks) rotary_side<T, C, P, LANES, INTERLEAVED, STREAM, 1>(p, block - p.q_blocks, turns);
+    else rotary_side<T, C, P, LANES, INTERLEAVED, STREAM, 2>(p, block - p.q_blocks - p.kv_blocks, turns);
+}
+
+// Any dims and pairs: 8 dims a lane, each of which finds its partner in LDS, where the row lies in fp32; the last
+// lane of a row may have fewer.  All of a row is read before any of it is written, which may be in its place.
+template <typename T, typename C, int LANES, int SIDE>
+__device__ __forceinline__ void rotary_side_any(const RotaryParams &p, int block, float *rows, float2 *turns) {
     const RotaryArgs &a = p.a;
-    const int64_t token = p.token + (int64_t)blockIdx.x;
-    fill_turns(p, turns, token, 1);
-    const int lane = (int)threadIdx.x % 64, wave = (int)threadIdx.x / 64, pairs = a.rotary.pairs;
-    float *const mine = rows[wave];
-    for (int r = wave; r < (int)p.rows.d; r += 4) {
-        const Row<T> row(p, token, r);
-        if (row.side != 0 && row.at < 0) continue;
-        float x[kEach];
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int d = lane + 64 * i;
-            x[i] = d < a.dim ? Value<T>::load1(row.from + d) : 0.f;
-            mine[d] = x[i];
+    const int teams = (int)blockDim.x / LANES;
+    const int each = SIDE == 0 ? p.q_tokens : p.kv_tokens, heads = SIDE == 0 ? a.heads : a.kv_heads;
+    const int64_t token0 = p.token + (int64_t)block * each;
+    const int tokens = (int)min((int64_t)each, p.end - token0), tasks = tokens * heads;
+    const FastDiv &by_heads = SIDE == 0 ? p.q_heads : p.kv_heads;
+    const int64_t token_step = SIDE == 0 ? a.q_token : SIDE == 1 ? a.k_token : a.v_token;
+    const int64_t head_step = SIDE == 0 ? a.q_head : SIDE == 1 ? a.k_head : a.v_head;
+    const T *const from = (const T *)(SIDE == 0 ? a.q : SIDE == 1 ? a.k : a.v) + token0 * token_step;
+    const int lane = (int)threadIdx.x % LANES, pairs = a.rotary.pairs, team = (int)threadIdx.x / LANES, d = 8 * lane;
+    float *const mine = rows + team * LANES * 8;
+
+    Held<T> next = {};
+    uint32_t next_slot = 0;
+    auto take = [&](int i) {
+        const int t = (int)by_heads.div((uint32_t)i), h = i - t * heads;
+        next = Held<T>(load_chunk<false>(from + t * token_step + h * head_step, d, a.dim));
+        if constexpr (SIDE != 0) next_slot = (uint32_t)a.slots[token0 + t];
+    };
+    if (team < tasks) take(team);
+    if constexpr (SIDE != 2) {
+        for (int i = (int)threadIdx.x; i < tokens * pairs; i += (int)blockDim.x) {
+            const int t = (int)p.pairs.div((uint32_t)i);
+            turns[i] = turn_of(a.rotary, a.positions[token0 + t], i - t * pairs);
         }
-        __builtin_amdgcn_wave_barrier();
+        __syncthreads();
+    }
+    for (int i = team; i < tasks; i += teams) {
+        f32x8 x = next.get();
+        const uint32_t slot = next_slot;
+        if (i + teams < tasks) take(i + teams);
+        const int t = (int)by_heads.div((uint32_t)i), h = i - t * heads;
+        if constexpr (SIDE != 2) {
+            const float2 *const by = turns + t * pairs;
+            if (a.rotary.interleaved) {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int d = lane + 64 * i;
-            if (row.side != 2 && d < 2 * pairs) {
-                const bool second = a.rotary.interleaved ? d % 2 != 0 : d >= pairs;
-                const int pair = a.rotary.interleaved ? d / 2 : second ? d - pairs : d;
-                const float other = mine[a.rotary.interleaved ? d ^ 1 : second ? pair : d + pairs];
-                float u = second ? other : x[i], v = second ? x[i] : other;
-                turn(u, v, turns[pair]);
-                x[i] = second ? v : u;
+                for (int e = 0; e < 4; ++e)
+                    if (d / 2 + e < pairs) {
+                        float u = x[2 * e], v = x[2 * e + 1];
+                        turn(u, v, by[d / 2 + e]);
+                        x[2 * e] = u, x[2 * e + 1] = v;
+                    }
+            } else {
+                *(f32x4 *)(mine + d) = f32x4{x[0], x[1], x[2], x[3]};
+                *(f32x4 *)(mine + d + 4) = f32x4{x[4], x[5], x[6], x[7]};
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int at = d + e;
+                    if (at >= 2 * pairs) continue;
+                    const bool second = at >= pairs;
+                    const float other = mine[second ? at - pairs : at + pairs];
+                    float u = second ? other : x[e], v = second ? x[e] : other;
+                    turn(u, v, by[second ? at - pairs : at]);
+                    x[e] = second ? v : u;
+                }
+                __builtin_amdgcn_wave_barrier();
             }
-            top = max(top, magnitude(x[i]));
         }
-        __builtin_amdgcn_wave_barrier();
-        if (row.side == 0) {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (lane + 64 * i < a.dim) Value<T>::store1(row.to + lane + 64 * i, x[i]);
-            continue;
-        }
-        C *const to = (C *)(row.side == 1 ? a.cache.k : a.cache.v) + row.at * a.dim;
-        if constexpr (std::is_same_v<C, int8_t>) {
-#pragma unroll
-            for (int o = 1; o < 64; o *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
-            const float s = row_scale(top), inv = row_inverse(s, top);
-            const f32x8 all = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
-            int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (inv != 0.f) row_codes8(all, s, inv, c);
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (lane + 64 * i < a.dim) to[lane + 64 * i] = (int8_t)c[i];
-            if (lane == 0) (row.side == 1 ? a.cache.k_scale : a.cache.v_scale)[row.at] = s;
+        if constexpr (SIDE == 0) {
+            T *const to = (T *)a.q_out + token0 * a.out_token + t * a.out_token + h * a.out_head;
+            if (d < a.dim) Held<T>(x).template store<false>(to, d, a.dim);
         } else {
+            if (slot >= p.slots) continue;  // negative slots are large numbers here
+            const int64_t line = cache_line(p, slot, h);
+            C *const to = (C *)(SIDE == 1 ? a.cache.k : a.cache.v) + line * a.dim + d;
+            if constexpr (std::is_same_v<C, int8_t>) {
+                uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (lane + 64 * i < a.dim) Value<C>::store1(to + lane + 64 * i, x[i]);
+                for (int e = 0; e < 8; ++e) top = max(top, magnitude(x[e]));
+                top = team_max_of<LANES>(top);
+                const float s = row_scale(top), inv = row_inverse(s, top);
+                int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (inv != 0.f) row_codes8(x, s, inv, c);
+                // a cache's rows are whole 8s
+                if (d < a.dim) *(u32x2 *)to = u32x2{pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])};
+                if (lane == 0) (SIDE == 1 ? a.cache.k_scale : a.cache.v_scale)[line] = s;
+            } else {
+                if (d < a.dim) Value<C>::store8(to, x);
+            }
         }
     }
 }
 
-template <typename T, typename C, int LANES, bool INTERLEAVED> void launch_pieces(const RotaryParams &p, int64_t tokens, hipStream_t st) {
-    RotaryParams q = p;
-    const int64_t each = (int64_t)p.rows.d * LANES;  // threads to a token
-    q.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(256 / each, 8));
-    const int threads = (int)std::min<int64_t>(kMostThreads, (q.tokens * each + 63) / 64 * 64);
-    rotary_pieces<T, C, LANES, INTERLEAVED><<<(unsigned)((tokens + q.tokens - 1) / q.tokens), threads,
-                                              q.tokens * p.a.rotary.pairs * sizeof(float2), st>>>(q);
+template <typename T, typename C, int LANES> __global__ __launch_bounds__(kMostThreads) void rotary_any(const RotaryParams p) {
+    extern __shared__ __attribute__((aligned(16))) float2 turns[];
+    __shared__ __attribute__((aligned(16))) float rows[kMostThreads * 8];
+    const int block = (int)blockIdx.x;
+    if (block < p.q_blocks) rotary_side_any<T, C, LANES, 0>(p, block, rows, turns);
+    else if (block < p.q_blocks + p.kv_blocks) rotary_side_any<T, C, LANES, 1>(p, block - p.q_blocks, rows, turns);
+    else rotary_side_any<T, C, LANES, 2>(p, block - p.q_blocks - p.kv_blocks, rows, turns);
 }
-template <typename T, typename C, int LANES> void launch_lanes(const RotaryParams &p, int64_t tokens, hipStream_t st) {
-    if (p.a.rotary.interleaved) launch_pieces<T, C, LANES, true>(p, tokens, st);
-    else launch_pieces<T, C, LANES, false>(p, tokens, st);
+
+// How a launch of teams of LANES lanes is divided.
+struct Division {
+    unsigned grid;
+    int threads;
+    size_t lds;
+};
+Division divide(RotaryParams &q, int64_t tokens, int lanes) {
+    const RotaryArgs &a = q.a;
+    q.q_heads = make_fastdiv((uint32_t)std::max(1, a.heads)), q.kv_heads = make_fastdiv((uint32_t)std::max(1, a.kv_heads));
+    q.pairs = make_fastdiv((uint32_t)a.rotary.pairs);
+    // A team takes two rows one after the other where that leaves enough workgroups.  The threads of a
+    // workgroup: those that leave the fewest idle.
+    const int64_t rows = a.heads + 2 * (int64_t)a.kv_heads, turns = tokens * rows * lanes > 2 * 256 * 2048 ? 2 : 1;
+    const int64_t most = 4096 / a.rotary.pairs;  // tokens, by the angles' 32 KiB
+    auto share = [&](int64_t heads, int64_t threads) {
+        return (int)std::max<int64_t>(1, std::min<int64_t>(most, turns * threads / (heads * lanes)));
+    };
+    const int64_t first = std::max(1, a.heads ? a.heads : a.kv_heads);
+    int threads = 0;
+    double best = 0;
+    for (int n : {256, 320, 384, 448, 512, 192}) {
+        const int64_t busy_lanes = share(first, n) * first * lanes;
+        const double busy = (double)busy_lanes / (double)((busy_lanes + n - 1) / n * n);
+        if (busy > best + 0.02) best = busy, threads = n;
+    }
+    q.q_tokens = share(std::max(1, a.heads), threads), q.kv_tokens = share(std::max(1, a.kv_heads), threads);
+    q.q_blocks = a.heads ? (int)((tokens + q.q_tokens - 1) / q.q_tokens) : 0;
+    q.kv_blocks = a.kv_heads ? (int)((tokens + q.kv_tokens - 1) / q.kv_tokens) : 0;
+    const int at_once = std::max(a.heads ? q.q_tokens : 0, a.kv_heads ? q.kv_tokens : 0);
+    return Division{(unsigned)(q.q_blocks + 2 * q.kv_blocks), threads, at_once * a.rotary.pairs * sizeof(float2)};
+}
+template <typename T, typename C, int P, int LANES> void launch_pieces(RotaryParams p, int64_t tokens, hipStream_t st) {
+    const Division d = divide(p, tokens, LANES);
+    const int64_t bytes = tokens * (p.a.heads + 2 * (int64_t)p.a.kv_heads) * p.a.dim * 2 * (int64_t)sizeof(T);
+    if constexpr (P == 8) {
+        if (bytes > kCached) {
+            if (p.a.rotary.interleaved) rotary_pieces<T, C, P, LANES, true, true><<<d.grid, d.threads, d.lds, st>>>(p);
+            else rotary_pieces<T, C, P, LANES, false, true><<<d.grid, d.threads, d.lds, st>>>(p);
+            return;
+        }
+    }
+    if (p.a.rotary.interleaved) rotary_pieces<T, C, P, LANES, true, false><<<d.grid, d.threads, d.lds, st>>>(p);
+    else rotary_pieces<T, C, P, LANES, false, false><<<d.grid, d.threads, d.lds, st>>>(p);
+}
+template <typename T, typename C, int LANES> void launch_any(RotaryParams p, int64_t tokens, hipStream_t st) {
+    const Division d = divide(p, tokens, LANES);
+    rotary_any<T, C, LANES><<<d.grid, d.threads, d.lds, st>>>(p);
+}
+// Caches have dims up to 256.
+template <typename T, typename C, int P> void launch_by_dim(const RotaryParams &p, int64_t tokens, hipStream_t st) {
+    if (p.a.dim <= 128) launch_pieces<T, C, P, 64 / P>(p, tokens, st);
+    else if (p.a.dim <= 256) launch_pieces<T, C, P, 128 / P>(p, tokens, st);
+    else if constexpr (std::is_same_v<T, C> && P > 2) launch_pieces<T, C, P, 256 / P>(p, tokens, st);
 }
 
 template <typename T, typename C> hipError_t launch2(const RotaryArgs &a, hipStream_t st) {
-    const int rows = a.heads + 2 * a.kv_heads;
-    RotaryParams p{a, make_fastdiv((uint32_t)rows), make_fastdiv((uint32_t)std::max(1, a.cache.page_size)),
-                   (uint32_t)(a.kv_heads ? a.cache.pages * a.cache.page_size : 0), 0, 0, 1};
-    const bool pieces = a.dim % 8 == 0 && (a.rotary.interleaved || a.rotary.pairs % 8 == 0);
+    RotaryParams p{a, make_fastdiv((uint32_t)std::max(1, a.cache.page_size)),
+                   (uint32_t)(a.kv_heads ? a.cache.pages * a.cache.page_size : 0), 0, 0};
+    // the largest pieces that dims and, of halves, pairs are whole numbers of
+    auto whole = [&](int n) { return a.dim % n == 0 && (a.rotary.interleaved || a.rotary.pairs % n == 0); };
+    const int piece = whole(8) ? 8 : whole(4) ? 4 : whole(2) && a.dim <= 256 ? 2 : 1;
     // one launch but for the largest calls: a launch holds fewer than 2^32 threads
     constexpr int64_t kMost = 1 << 21;
     for (; p.token < a.tokens; p.token += kMost) {
         const int64_t tokens = std::min(kMost, a.tokens - p.token);
         p.end = p.token + tokens;
-        if (!pieces) rotary_values<T, C><<<(unsigned)tokens, 256, 0, st>>>(p);
-        else if (a.dim <= 128) launch_lanes<T, C, 8>(p, tokens, st);
-        else if (a.dim <= 256) launch_lanes<T, C, 16>(p, tokens, st);
-        else if constexpr (std::is_same_v<T, C>) launch_lanes<T, C, 32>(p, tokens, st);
+        if (piece == 8) launch_by_dim<T, C, 8>(p, tokens, st);
+        else if (piece == 4) launch_by_dim<T, C, 4>(p, tokens, st);
+        else if (piece == 2) launch_by_dim<T, C, 2>(p, tokens, st);
+        else if (a.dim <= 128) launch_any<T, C, 16>(p, tokens, st);
+        else if (a.dim <= 256) launch_any<T, C, 32>(p, tokens, st);
+        else if constexpr (std::is_same_v<T, C>) launch_any<T, C, 64>(p, tokens, st);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
