@@ -75,23 +75,23 @@ class Rows8:
     """
 
     def __init__(self, buffer, shape, dtype):
-        self.buffer, self.shape, self.dtype = buffer, torch.Size(shape), dtype
-        self._lead, self._k = tuple(self.shape[:-1]), self.shape[-1]
-        self._rows = math.prod(self._lead)
+        self.buffer, self.shape, self.dtype = buffer, shape, dtype
 
     def _split(self):
-        r = (self._rows + 15) // 16 * 16
-        return self.buffer[:4 * r].view(torch.float32), self.buffer[4 * r:].view((self._k + 127) // 128 * 2, r, 64)
+        r, blocks = (math.prod(self.shape[:-1]) + 15) // 16 * 16, (self.shape[-1] + 127) // 128 * 2
+        return self.buffer[:4 * r].view(torch.float32), self.buffer[4 * r:].view(blocks, r, 64)
 
     @property
     def scale(self):
         """float32 [...], in the buffer."""
-        return self._split()[0][:self._rows].view(self._lead)
+        lead = self.shape[:-1]
+        return self._split()[0][:math.prod(lead)].view(lead)
 
     @property
     def codes(self):
         """int8 [..., K], a copy."""
-        return self._split()[1].transpose(0, 1).flatten(1)[:self._rows, :self._k].reshape(self.shape)
+        rows = self._split()[1].transpose(0, 1).flatten(1)
+        return rows[:math.prod(self.shape[:-1]), :self.shape[-1]].reshape(self.shape)
 
     def dequantize(self, dtype=None):
         """codes * scale, a copy of `dtype` (that of what they were made of by default)."""
@@ -108,7 +108,7 @@ def int8_linear(x, w, w_scale, bias=None, activation=None, out=None, library: Li
     "silu".  Returns [..., N] of x's type.  x may be ``Rows8``, quantised already.
     """
     if type(x) is Rows8:
-        return _checked(_block8.int8_linear_rows(_handle(library), x.buffer, x._rows, x._k, x.dtype, x._lead, w, w_scale, bias,
+        return _checked(_block8.int8_linear_rows(_handle(library), x.buffer, x.shape, x.dtype, w, w_scale, bias,
                                                  ACTIVATIONS.get(activation, -1), out), library, "cbs_int8_linear_rows")
     return _checked(_block8.int8_linear(_handle(library), x, w, w_scale, bias, ACTIVATIONS.get(activation, -1), out),
                     library, "cbs_int8_linear")

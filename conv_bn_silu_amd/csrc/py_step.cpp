@@ -84,42 +84,42 @@ PyObject *add_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// (handle, buffer, M, K, dtype, leading shape, w, w_scale, bias, activation, out)
+// (handle, buffer, shape, dtype, w, w_scale, bias, activation, out)
 PyObject *int8_linear_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 11, [&]() -> PyObject * {
+    return guarded(n, 9, [&]() -> PyObject * {
         const at::Tensor &rows = tensor(a[1], "rows", {at::kChar});
         on_current_device(rows, "rows");
-        const int64_t M = whole(a[2]), K = whole(a[3]);
-        const at::ScalarType type = value_dtype(a[4], "dtype");
-        const at::Tensor &w = tensor(a[6], "w", {at::kChar}, &rows);
-        const at::Tensor &ws = tensor(a[7], "w_scale", {at::kFloat}, &rows);
+        if (!PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) < 1) refuse(PyExc_TypeError, "the rows' shape must be a tuple, [..., K]");
+        c10::SmallVector<int64_t, 8> shape;
+        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[2]); ++i) shape.push_back(whole(PyTuple_GET_ITEM(a[2], i)));
+        const int64_t K = shape.back();
+        int64_t M = 1;
+        for (size_t i = 0; i + 1 < shape.size(); ++i) {
+            if (shape[i] < 0 || (shape[i] > 0 && M > INT32_MAX / shape[i])) refuse(PyExc_ValueError, "the rows' shape cannot be");
+            M *= shape[i];
+        }
+        const at::ScalarType type = value_dtype(a[3], "dtype");
+        const at::Tensor &w = tensor(a[4], "w", {at::kChar}, &rows);
+        const at::Tensor &ws = tensor(a[5], "w_scale", {at::kFloat}, &rows);
         if (w.dim() != 2 || w.size(1) != K) refuse(PyExc_ValueError, "x must be [..., K] and w [N, K]");
-        const int act = (int)whole(a[9]);
+        const int act = (int)whole(a[7]);
         if (act < 0) refuse(PyExc_ValueError, "activation must be None or 'silu'");
         const int64_t N = w.size(0);
         contiguous(w, {N, K}, "w");
         contiguous(ws, {N}, "w_scale");
         contiguous(rows, {bytes_of(cbs_rows8_bytes(M, K))}, "rows");
         const void *bias = nullptr;
-        if (a[8] != Py_None) {
-            const at::Tensor &b = tensor(a[8], "bias", {at::kFloat}, &rows);
+        if (a[6] != Py_None) {
+            const at::Tensor &b = tensor(a[6], "bias", {at::kFloat}, &rows);
             contiguous(b, {N}, "bias");
             bias = b.data_ptr();
         }
-        if (!PyTuple_Check(a[5])) refuse(PyExc_TypeError, "the leading shape must be a tuple");
-        c10::SmallVector<int64_t, 8> shape;
-        int64_t lead = 1;
-        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[5]); ++i) {
-            shape.push_back(whole(PyTuple_GET_ITEM(a[5], i)));
-            lead *= shape.back();
-        }
-        if (lead != M) refuse(PyExc_ValueError, "the leading shape does not hold the rows");
-        shape.push_back(N);
+        shape.back() = N;
         at::Tensor y;
-        if (a[10] == Py_None) {
+        if (a[8] == Py_None) {
             y = at::empty(shape, rows.options().dtype(type).requires_grad(false));
         } else {
-            y = tensor(a[10], "out", {type}, &rows);
+            y = tensor(a[8], "out", {type}, &rows);
             contiguous(y, shape, "out");
         }
         const int64_t need = cbs_int8_linear_rows_workspace(M, N, K);

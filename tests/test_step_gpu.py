@@ -153,7 +153,7 @@ def test_norm_strides_places_and_shapes(ops, K):
 
 def test_norm_rows_leave_their_padding(ops):
     """What a buffer holds for rows past M, and past it, is not written."""
-    from conv_bn_silu_amd import binding as B
+    from conv_bn_silu_amd import binding as B, step  # noqa: F401  (declares the types)
     M, K = 5, 200
     x, w, _ = norm_inputs(M, K, BF16, None, BF16, 2)
     x, w = x.cuda(), w.cuda()
