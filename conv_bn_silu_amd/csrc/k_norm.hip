@@ -8,9 +8,12 @@
 // Rows beyond 8192 take 16 values a lane, those beyond 16384 read h a second time.  What the memory-side cache cannot
 // hold passes by the caches (180 -> 170 us; outputs in 8 bits stay, for the layer reads them: 8192 x 8192 with
 // what is read passing by as well 220 us into a layer of 1024, without 214), and eight workgroups of neighbouring rows
-// share an XCD (172 -> 169).  Together 168 us, 6.4 TB/s.
-//   Rows of 1024 (131072 of them) 172 us for 170, of 256 (300000) 99 for 98, of 128 (a million, no residual) 90
-//   for 85; 16384 wide 173 for 170; 32768 wide 206 for 170; one row of 4096: 2.8 us on the GPU, 6 a call.
+// share an XCD (172 -> 169).  Together 170 us, 6.3 TB/s.
+//   Rows of 1024 (131072 of them) 171 us for 170, of 256 (300000) 98 for 98, of 128 (a million, no residual) 85
+//   for 85; 16384 wide 173 for 170; 32768 wide 209 for 170; one row of 4096: 2.8 us on the GPU, 5 to 6 a call.
+// With 8 bits the vector unit counts as well (450 instructions for a lane's 8 values at first, 87% of the time):
+// sizes of whole 8s have no ragged ends, and codes come out of one fused addition each.  8192 x 8192, bf16 with
+// residual: 104 -> 93 us (537 MB: 75), of 16384 253 -> 168 (149); residual in fp32 118 (738 MB: 117).
 //
 // Squares are summed in 64 bits: no row of finite numbers overflows or vanishes on the way.
 #include <hip/hip_runtime.h>
@@ -38,26 +41,33 @@ __device__ __forceinline__ double reciprocal_root(double s) {
     return s == INFINITY ? 0.0 : better;
 }
 
+// 8 values of a row from k on.  FULL: K is a whole number of 8s, so that nothing is ragged.
+template <bool FULL, bool STREAM, typename T> __device__ __forceinline__ Held<T> take(const T *row, int k, int K) {
+    if constexpr (FULL) return k < K ? Held<T>::template load<STREAM>(row + k) : Held<T>{};
+    else return Held<T>(load_chunk<STREAM>(row, k, K));
+}
+template <bool FULL, bool STREAM, typename T> __device__ __forceinline__ void put(T *row, int k, int K, const Held<T> &v) {
+    if constexpr (FULL) store_held<STREAM>(row + k, v);
+    else v.template store<STREAM>(row, k, K);
+}
+
 // 8 weights on their way: they are asked for before the sum of squares, and wanted after it.  Wide ones beside
 // narrow values are not, for the registers they take would cost more than the wait.
-template <typename T> struct Weights {
-    u32x4 raw[sizeof(T) / 2];
+template <typename T, bool FULL> struct Weights {
+    Held<T> held;
     __device__ __forceinline__ void load(const NormArgs &a, int k) {
-        if (k + 8 > a.K || !a.weight || a.weight_dtype != a.dtype) return;
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) raw[i] = ((const Any16 *)((const T *)a.weight + k))[i].v;
+        if (a.weight && a.weight_dtype == a.dtype) held = take<FULL, false>((const T *)a.weight, k, a.K);
     }
     __device__ __forceinline__ f32x8 get(const NormArgs &a, int k) const {
         if (!a.weight) return f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-        if (a.weight_dtype != a.dtype) return load_chunk<false>((const float *)a.weight, k, a.K);
-        return k + 8 > a.K ? load_chunk<false>((const T *)a.weight, k, a.K) : Held<T>{raw}.get();
+        return a.weight_dtype == a.dtype ? held.get() : take<FULL, false>((const float *)a.weight, k, a.K).get();
     }
 };
 
 // T: type of x and y, R: of the residual and the sum.  TEAM lanes to a row; teams of 128 and less share a
 // workgroup of 256, or a row has a workgroup (TEAM 0).  CHUNKS: of 8 values a lane keeps.  STREAM: the tensors pass by
 // the caches.
-template <typename T, typename R, int TEAM, int CHUNKS, bool INT8, bool STREAM>
+template <typename T, typename R, int TEAM, int CHUNKS, bool INT8, bool FULL, bool STREAM>
 __global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormParams p) {
     constexpr int kLanes = TEAM == 0 || TEAM > 64 ? 64 : TEAM, kMostWaves = TEAM ? 4 : 16;
     constexpr bool kMeet = TEAM == 0 || TEAM > 64;  // a row's waves meet in LDS
@@ -65,26 +75,25 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormPara
     __shared__ double squares_of[kMostWaves];
     __shared__ uint32_t top_of[kMostWaves];
     const NormArgs &a = p.a;
-    const int team = TEAM ? TEAM : (int)blockDim.x, tid = (int)threadIdx.x, lane = tid % team, K = a.K;
+    const int team = TEAM ? TEAM : (int)blockDim.x, tid = (int)threadIdx.x, lane = TEAM ? tid % TEAM : tid, K = a.K;
     // workgroups go to the eight XCDs in turn; of 64, each gets 8 with rows side by side
     const int id = (int)blockIdx.x, group = id & ~63, in = id & 63;
     const int place = group + 64 <= (int)gridDim.x ? group + in % 8 * 8 + in / 8 : id;
     int m = p.m0 + (TEAM ? place * (256 / team) + tid / team : place);
-    const bool mine = m < a.M;
+    const bool mine = TEAM == 0 || m < a.M;
     if (!kMeet && !mine) return;
-    m = min(m, a.M - 1);  // reads the last row and writes nothing
+    if (TEAM) m = min(m, a.M - 1);  // reads the last row and writes nothing
     const T *const x = (const T *)a.x + (int64_t)m * a.x_stride;
     const R *const residual = a.residual ? (const R *)a.residual + (int64_t)m * a.residual_stride : nullptr;
     R *const sum = (R *)a.sum + (int64_t)m * a.sum_stride;
     const int end = mine ? K : 0, code_end = mine ? p.l.Kp : 0;  // of what is written
 
-    auto add = [&](f32x8 h, f32x8 r, int k) {
-        h += r;
-        const Held<R> v(h);
-        if (k < end) v.template store<STREAM>(sum, k, K);
+    auto add = [&](const Held<T> &h, const Held<R> &r, int k) {
+        const Held<R> v(h.get() + r.get());
+        if (k < end) put<FULL, STREAM>(sum, k, K, v);
         return v;
     };
-    auto again = [&](int k) { return residual ? load_chunk<false>(sum, k, K) : load_chunk<false>(x, k, K); };
+    auto again = [&](int k) { return residual ? take<FULL, false>((const R *)sum, k, K).get() : take<FULL, false>(x, k, K).get(); };
     auto square = [&](double &to, f32x8 h) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) to = __builtin_fma((double)h[i], (double)h[i], to);
@@ -92,15 +101,15 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormPara
     const int span = CHUNKS * team * 8;
     // h is a number of R's with a residual, of T's without, which R holds too
     Held<R> keep[CHUNKS];
-    Weights<T> weights[CHUNKS];
+    Weights<T, FULL> weights[CHUNKS];
     {
-        f32x8 h[CHUNKS];
+        Held<T> h[CHUNKS];
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) h[c] = load_chunk<kOnce>(x, (c * team + lane) * 8, K);
+        for (int c = 0; c < CHUNKS; ++c) h[c] = take<FULL, kOnce>(x, (c * team + lane) * 8, K);
         if (residual) {
-            f32x8 r[CHUNKS];
+            Held<R> r[CHUNKS];
 #pragma unroll
-            for (int c = 0; c < CHUNKS; ++c) r[c] = load_chunk<kOnce>(residual, (c * team + lane) * 8, K);
+            for (int c = 0; c < CHUNKS; ++c) r[c] = take<FULL, kOnce>(residual, (c * team + lane) * 8, K);
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) weights[c].load(a, (c * team + lane) * 8);
 #pragma unroll
@@ -109,15 +118,15 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormPara
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) weights[c].load(a, (c * team + lane) * 8);
 #pragma unroll
-            for (int c = 0; c < CHUNKS; ++c) keep[c] = Held<R>(h[c]);
+            for (int c = 0; c < CHUNKS; ++c) keep[c] = Held<R>(h[c].get());
         }
     }
     double part[CHUNKS] = {}, squares = 0;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) square(part[c], keep[c].get());
     for (int k = span + lane * 8; k < K; k += team * 8) {
-        const f32x8 h = load_chunk<false>(x, k, K);
-        square(squares, residual ? add(h, load_chunk<false>(residual, k, K), k).get() : h);
+        const Held<T> h = take<FULL, false>(x, k, K);
+        square(squares, residual ? add(h, take<FULL, false>(residual, k, K), k).get() : h.get());
     }
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) squares += part[c];
@@ -133,19 +142,17 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormPara
     // h r in fp32 with one rounding: r in two parts, and where it comes near fp32's smallest numbers h and r
     // meet half way
     double r = reciprocal_root(__builtin_fma(squares, p.inv_k, (double)a.eps));
-    const float fit = r < 0x1p-64 ? 0x1p-64f : 1.f;
-    if (r < 0x1p-64) r *= 0x1p64;
+    const bool small = r < 0x1p-64;
+    if (small) r *= 0x1p64;
     const float r_hi = (float)r, r_lo = (float)(r - (double)r_hi);
     auto scaled = [&](f32x8 h, f32x8 w) {
+        if (__builtin_expect(small, 0)) h *= 0x1p-64f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float v = h[i] * fit;
-            h[i] = __builtin_fmaf(v, r_hi, v * r_lo) * w[i];
-        }
+        for (int i = 0; i < 8; ++i) h[i] = __builtin_fmaf(h[i], r_hi, h[i] * r_lo) * w[i];
         return h;
     };
     auto scaled_again = [&](int k) {
-        Weights<T> w;
+        Weights<T, FULL> w;
         w.load(a, k);
         return scaled(again(k), w.get(a, k));
     };
@@ -154,9 +161,9 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormPara
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
             const int k = (c * team + lane) * 8;
-            if (k < end) Held<T>(scaled(keep[c].get(), weights[c].get(a, k))).template store<STREAM>(y, k, K);
+            if (k < end) put<FULL, STREAM>(y, k, K, Held<T>(scaled(keep[c].get(), weights[c].get(a, k))));
         }
-        for (int k = span + lane * 8; k < end; k += team * 8) Held<T>(scaled_again(k)).template store<STREAM>(y, k, K);
+        for (int k = span + lane * 8; k < end; k += team * 8) put<FULL, STREAM>(y, k, K, Held<T>(scaled_again(k)));
     } else {
         uint32_t top = 0;
         auto largest = [&](f32x8 y) {
@@ -180,12 +187,10 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormPara
             __syncthreads();
             top = team_max_of<TEAM ? 2 : 16>(there ? top_of[its] : 0u);
         }
-        const float s = row_scale(top), inv = row_inverse(s, top);
+        // the quotient is off by less than 4e-5 with the instruction's reciprocal, too
+        const float s = row_scale(top), inv = top >= 0x7F800000u ? 0.f : __builtin_amdgcn_rcpf(s);
         auto codes = [&](f32x8 y, int k) {
-            int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (inv != 0.f) row_codes8(y, s, inv, c);
-            *(u32x2 *)(p.l.codes + ((int64_t)(k >> 6) * p.l.rows + m) * 64 + (k & 63)) =
-                u32x2{pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])};
+            *(u32x2 *)(p.l.codes + ((int64_t)(k >> 6) * p.l.rows + m) * 64 + (k & 63)) = inv != 0.f ? codes_of8(y, s, inv) : u32x2{0u, 0u};
         };
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
@@ -199,7 +204,7 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormPara
     }
 }
 
-template <typename T, typename R, int TEAM, int CHUNKS, bool INT8, bool STREAM>
+template <typename T, typename R, int TEAM, int CHUNKS, bool INT8, bool FULL, bool STREAM>
 hipError_t launch5(const NormArgs &a, const CodesLayout &l, hipStream_t st) {
     const int rows = TEAM ? 256 / TEAM : 1, threads = TEAM ? 256 : std::min(1024, (a.K + 512 * CHUNKS - 1) / (512 * CHUNKS) * 64);
     // one launch but for the largest sizes: a launch holds fewer than 2^32 threads
@@ -208,14 +213,15 @@ hipError_t launch5(const NormArgs &a, const CodesLayout &l, hipStream_t st) {
     for (int m0 = 0; m0 < a.M && e == hipSuccess; m0 += kMost) {
         const NormParams p{a, l, m0, 1.0 / a.K};
         const unsigned grid = (unsigned)((std::min(kMost, a.M - m0) + rows - 1) / rows);
-        add_rms_norm<T, R, TEAM, CHUNKS, INT8, STREAM><<<grid, threads, 0, st>>>(p);
+        add_rms_norm<T, R, TEAM, CHUNKS, INT8, FULL, STREAM><<<grid, threads, 0, st>>>(p);
         e = hipGetLastError();
     }
     return e;
 }
 template <typename T, typename R, int TEAM, int CHUNKS, bool INT8> hipError_t launch4(const NormArgs &a, const CodesLayout &l, hipStream_t st) {
+    if (a.K % 8 != 0) return launch5<T, R, TEAM, CHUNKS, INT8, false, false>(a, l, st);
     const int64_t bytes = (int64_t)a.M * a.K * ((a.int8 ? 1 : 2) * sizeof(T) + (a.residual ? 2 * sizeof(R) : 0));
-    return bytes > kCached ? launch5<T, R, TEAM, CHUNKS, INT8, true>(a, l, st) : launch5<T, R, TEAM, CHUNKS, INT8, false>(a, l, st);
+    return bytes > kCached ? launch5<T, R, TEAM, CHUNKS, INT8, true, true>(a, l, st) : launch5<T, R, TEAM, CHUNKS, INT8, true, false>(a, l, st);
 }
 template <typename T, typename R, bool INT8> hipError_t launch3(const NormArgs &a, const CodesLayout &l, hipStream_t st) {
     if (a.K <= 128) return launch4<T, R, 16, 1, INT8>(a, l, st);
