@@ -187,8 +187,7 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void add_rms_norm(const NormPara
             __syncthreads();
             top = team_max_of<TEAM ? 2 : 16>(there ? top_of[its] : 0u);
         }
-        // the quotient is off by less than 4e-5 with the instruction's reciprocal, too
-        const float s = row_scale(top), inv = top >= 0x7F800000u ? 0.f : __builtin_amdgcn_rcpf(s);
+        const float s = row_scale(top), inv = row_quotient(s, top);
         auto codes = [&](f32x8 y, int k) {
             *(u32x2 *)(p.l.codes + ((int64_t)(k >> 6) * p.l.rows + m) * 64 + (k & 63)) = inv != 0.f ? codes_of8(y, s, inv) : u32x2{0u, 0u};
         };

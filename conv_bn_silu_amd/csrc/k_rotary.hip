@@ -172,24 +172,17 @@ __device__ __forceinline__ void rotary_side(const RotaryParams &p, int block, fl
 #pragma unroll
                 for (int e = 0; e < 2 * P; ++e) top = max(top, magnitude(x[e]));
                 top = team_max_of<LANES>(top);
-                const float s = row_scale(top), inv = row_inverse(s, top);
-                int c[16] = {};
-                if (inv != 0.f) {
+                const float s = row_scale(top), inv = row_quotient(s, top);
+                u32x2 codes[2] = {};
 #pragma unroll
-                    for (int g = 0; g < (2 * P + 7) / 8; ++g) {
-                        f32x8 v = {};
+                for (int g = 0; g < (2 * P + 7) / 8; ++g) {
+                    f32x8 v = {};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (8 * g + e < 2 * P) v[e] = x[8 * g + e];
-                        int eight[8];
-                        row_codes8(v, s, inv, eight);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) c[8 * g + e] = eight[e];
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        if (8 * g + e < 2 * P) v[e] = x[8 * g + e];
+                    if (inv != 0.f) codes[g] = codes_of8(v, s, inv);
                 }
                 if constexpr (P == 8) {
-                    const u32x2 codes[2] = {{pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])},
-                                            {pack_codes(c[8], c[9], c[10], c[11]), pack_codes(c[12], c[13], c[14], c[15])}};
                     // pieces that lie apart: two lanes exchange one each, for stores of 16 bytes
                     const bool odd = lane & 1, trade = !INTERLEAVED && lane < (half & ~1);
                     const u32x2 give = odd ? codes[0] : codes[1];
@@ -202,13 +195,12 @@ __device__ __forceinline__ void rotary_side(const RotaryParams &p, int block, fl
                         if (has1) *(u32x2 *)(to + d1) = codes[1];
                     }
                 } else {
-                    const uint32_t lo = pack_codes(c[0], c[1], c[2], c[3]), hi = pack_codes(c[4], c[5], c[6], c[7]);
                     if constexpr (P == 4) {
-                        if (has0) *(uint32_t *)(to + d0) = lo;
-                        if (has1) *(uint32_t *)(to + d1) = hi;
+                        if (has0) *(uint32_t *)(to + d0) = codes[0].x;
+                        if (has1) *(uint32_t *)(to + d1) = codes[0].y;
                     } else {
-                        if (has0) *(uint16_t *)(to + d0) = (uint16_t)lo;
-                        if (has1) *(uint16_t *)(to + d1) = (uint16_t)(lo >> 16);
+                        if (has0) *(uint16_t *)(to + d0) = (uint16_t)codes[0].x;
+                        if (has1) *(uint16_t *)(to + d1) = (uint16_t)(codes[0].x >> 16);
                     }
                 }
                 if (lane == 0) (SIDE == 1 ? a.cache.k_scale : a.cache.v_scale)[line] = s;
@@ -304,11 +296,9 @@ __device__ __forceinline__ void rotary_side_any(const RotaryParams &p, int block
 #pragma unroll
                 for (int e = 0; e < 8; ++e) top = max(top, magnitude(x[e]));
                 top = team_max_of<LANES>(top);
-                const float s = row_scale(top), inv = row_inverse(s, top);
-                int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (inv != 0.f) row_codes8(x, s, inv, c);
+                const float s = row_scale(top), inv = row_quotient(s, top);
                 // a cache's rows are whole 8s
-                if (d < a.dim) *(u32x2 *)to = u32x2{pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])};
+                if (d < a.dim) *(u32x2 *)to = inv != 0.f ? codes_of8(x, s, inv) : u32x2{0u, 0u};
                 if (lane == 0) (SIDE == 1 ? a.cache.k_scale : a.cache.v_scale)[line] = s;
             } else {
                 if (d < a.dim) Value<C>::store8(to, x);

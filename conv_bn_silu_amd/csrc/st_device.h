@@ -141,6 +141,12 @@ template <int TEAM> __device__ __forceinline__ uint32_t team_sum_of(uint32_t v) 
     return over_team<TEAM>(v, [](uint32_t a, auto &&other) { return a + other(a); });
 }
 
+// A row's factor of the quotients, by the instruction's reciprocal (good to 1 ulp, which is enough for the codes); 0
+// where the row holds an infinity or a NaN and gets the codes 0.
+__device__ __forceinline__ float row_quotient(float s, uint32_t amax_bits) {
+    return amax_bits >= 0x7F800000u ? 0.f : __builtin_amdgcn_rcpf(s);
+}
+
 // Codes of 8 values of a row as row_codes8 (b8_device.h) has them, packed, in fewer instructions: adding 1.5 2^23 leaves
 // the nearest whole number to x inv, ties to even, in the sum's low bits, and the distance from it says whether x lies
 // so near a border that the remainder has to be looked at.  For |x inv| below 2^21 (or no number at all).
