@@ -70,7 +70,7 @@ def _checked(got, library, what):
 class Rows8:
     """Rows in 8 bits, [..., K]: codes in [-127, 127], each row with a scale, as the linear layer makes
     them of its input and ``add_rms_norm`` gives them.  They lie as the layer's matrix kernels read them, in
-    one int8 tensor (`buffer`; the layout is in include/cbs_block8.h).  dtype: of what they were made of, and
+    one int8 tensor (`buffer`; the layout is in include/cbs_block8.h).  shape: a tuple, [..., K].  dtype: of what they were made of, and
     of the layer's output.
     """
 

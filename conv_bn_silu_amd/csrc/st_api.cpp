@@ -16,7 +16,7 @@ namespace {
 using namespace cbs;
 
 constexpr int64_t kMaxK = 131072, kMaxRows = 1 << 24;  // as the linear layer's
-constexpr int kMaxDim = 512;
+constexpr int kMaxDim = 512, kMaxHeads = 65536;
 
 // A tensor [tokens][heads][dim] as the rotary operators take it.
 struct Heads {
@@ -110,7 +110,7 @@ int cbs_rotary_apply(conv_bn_silu_t h, const cbs_rotary *rotary, const void *x, 
     if (!value_type(dtype) || tokens < 0 || heads < 1 || dim < 1) return CBS_ERR_INVALID_ARG;
     int rc = check_rotary(rotary, dim);
     if (rc != CBS_OK) return rc;
-    if (dim > kMaxDim || tokens > INT32_MAX / heads) return CBS_ERR_UNSUPPORTED;
+    if (dim > kMaxDim || heads > kMaxHeads || tokens > INT32_MAX / heads) return CBS_ERR_UNSUPPORTED;
     if (tokens == 0) return CBS_OK;
     if (!x || !out || !positions) return CBS_ERR_INVALID_ARG;
     rc = check_strides(tokens, heads, dim, token_stride, head_stride);
@@ -142,7 +142,7 @@ int cbs_rotary_cache_write(conv_bn_silu_t h, const cbs_rotary *rotary, const cbs
     if (!value_type(dtype) || tokens < 0 || heads < 0) return CBS_ERR_INVALID_ARG;
     rc = check_rotary(rotary, cache->dim);
     if (rc != CBS_OK) return rc;
-    if (tokens > INT32_MAX / ((int64_t)heads + 2 * cache->heads)) return CBS_ERR_UNSUPPORTED;
+    if (heads > kMaxHeads || tokens > INT32_MAX / ((int64_t)heads + 2 * cache->heads)) return CBS_ERR_UNSUPPORTED;
     if (tokens == 0) return CBS_OK;
     if (!k || !v || !positions || !slots || (heads > 0 && (!q || !q_out)) || !tensors_disjoint(*cache))
         return CBS_ERR_INVALID_ARG;

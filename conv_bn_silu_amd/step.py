@@ -106,7 +106,7 @@ def rotary(x, positions, frequencies, interleaved: bool = False, magnitude: floa
     """Heads turned by their tokens' positions: pair i becomes magnitude * (a cos t - b sin t, b cos t + a sin t)
     with t = position * frequencies[i].
 
-    x: [tokens, heads, dim] float32, bfloat16 or float16, dim (up to 512) contiguous; positions: int32
+    x: [tokens, heads, dim] float32, bfloat16 or float16, dim (up to 512) contiguous, heads up to 65536; positions: int32
     [tokens]; frequencies: float64 [pairs], 2 * pairs up to dim; pair i is (i, i + pairs), or
     (2i, 2i + 1) where `interleaved`; the dims past 2 * pairs stay as they are.  Queries and keys that lie side by
     side in a projection's output are turned in one call.

@@ -56,7 +56,7 @@ typedef struct cbs_rotary {
 /* out = x turned.  x, out: [tokens][heads][dim] of dtype (F32, BF16 or F16), token and head
  * strides in elements (at least dim), dim contiguous; positions: int32 [tokens], of any sign.
  * out may be x itself (the same pointer and strides), else it must not overlap x; its own rows
- * must not overlap.  2 * pairs <= dim <= 512, tokens * heads < 2^31. */
+ * must not overlap.  2 * pairs <= dim <= 512, heads <= 65536, tokens * heads < 2^31. */
 int cbs_rotary_apply(conv_bn_silu_t handle, const cbs_rotary *rotary, const void *x, int64_t token_stride,
                      int64_t head_stride, const int32_t *positions, int64_t tokens, int heads, int dim, int dtype,
                      void *out, int64_t out_token_stride, int64_t out_head_stride, void *stream);
@@ -69,7 +69,7 @@ int cbs_rotary_apply(conv_bn_silu_t handle, const cbs_rotary *rotary, const void
  *   whose slot lies outside the cache is not written (its queries are turned all the same), and no
  *   two tokens may name one slot.  q_out may be q itself; it may lie between other tensors' rows, as
  *   parts of one wider tensor do, but not on them.
- * 2 * pairs <= dim; tokens * (heads + 2 * cache heads) < 2^31. */
+ * 2 * pairs <= dim; heads <= 65536, tokens * (heads + 2 * cache heads) < 2^31. */
 int cbs_rotary_cache_write(conv_bn_silu_t handle, const cbs_rotary *rotary, const cbs_paged_cache *cache, const void *q,
                            int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,
                            int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,

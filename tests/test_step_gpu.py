@@ -710,6 +710,7 @@ def test_refusals(ops):
     long = torch.zeros(4, 4, 64, dtype=BF16, **dev)
     over = torch.zeros(3 * 64, dtype=BF16, **dev).as_strided((3, 4, 64), (64, 0, 1))
     for bad in (dict(x=long[:3], out=long[1:]), dict(x=torch.zeros(1, 1, 514, **dev), positions=pos[:1]), dict(out=over),
+                dict(x=torch.zeros(3, 65537, 2, **dev), frequencies=f[:1]),
                 dict(x=long[:3], out=long.view(-1)[8:8 + 768].view(3, 4, 64))):
         with pytest.raises(CbsError):
             ops.rotary(**{**dict(x=q, positions=pos, frequencies=f), **bad})
