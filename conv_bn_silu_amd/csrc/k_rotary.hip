@@ -7,13 +7,13 @@
 // angles out once, into LDS, while its first rows are on their way.
 //
 // Bound by HBM: every row is read once and written once.  32768 tokens, 32 heads over 8, dim 128, bf16 into
-// 8 bits: 134 us, 5.5 TB/s (740 MB; a large copy: 6.3 TB/s, 117 us).  Queries, keys and values go to different
+// 8 bits: 128 us, 5.8 TB/s (740 MB; a large copy: 6.3 TB/s, 117 us).  Queries, keys and values go to different
 // workgroups, whose addresses and branches are then the same for all lanes (a workgroup with all rows of
 // a token, each lane looking up its own: 185 us, 250 vector instructions a row of 16 lanes' values); a team takes two rows at
 // most, one after the other (eight: 146).  Other forms, us and what a copy would take: into 16 bits 145, 128;
-// fp32 into 8 bits 263, 224; dim 64 138, 101; 8 heads over 8 70, 53; 8192 tokens of 40 heads without
-// a cache 31, 27; 5001 ragged ones 9, 6; one or 64 tokens 3 on the GPU, 8 a call.  Pairs that are no whole 8
-// make smaller pieces: dim 80 with 20 pairs 140, 60; dim 100 with 50 118, 67 (any numbers, through LDS: 195 and 238).
+// fp32 into 8 bits 267, 224; dim 64 134, 101; dim 256 130, 117; 8 heads over 8 62, 53; 8192 tokens 37, 29; of 40 heads
+// without a cache 32, 27; 5001 ragged ones 10, 6; one or 64 tokens 3 on the GPU, 8 a call.  Pairs that are no whole 8
+// make smaller pieces: dim 80 with 20 pairs 133, 60; dim 100 with 50 120, 67 (any numbers, through LDS: 195 and 238).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -32,7 +32,8 @@ struct RotaryParams {
     FastDiv page;
     uint32_t slots;   // pages * page size
     int64_t token, end;  // tokens of the launch
-    // rotary_pieces: workgroups of the queries and of the keys (and of the values), tokens of each
+    // workgroups of the queries and of the keys (and of the values), tokens of each; the keys, whose workgroups take
+    // longest, go first (8192 tokens 43 -> 39 us)
     int q_blocks, kv_blocks, q_tokens, kv_tokens;
     FastDiv q_heads, kv_heads, pairs;
 };
@@ -216,9 +217,9 @@ template <typename T, typename C, int P, int LANES, bool INTERLEAVED, bool STREA
 __global__ __launch_bounds__(kMostThreads) void rotary_pieces(const RotaryParams p) {
     extern __shared__ __attribute__((aligned(16))) float2 turns[];
     const int block = (int)blockIdx.x;
-    if (block < p.q_blocks) rotary_side<T, C, P, LANES, INTERLEAVED, STREAM, 0>(p, block, turns);
-    else if (block < p.q_blocks + p.kv_blocks) rotary_side<T, C, P, LANES, INTERLEAVED, STREAM, 1>(p, block - p.q_blocks, turns);
-    else rotary_side<T, C, P, LANES, INTERLEAVED, STREAM, 2>(p, block - p.q_blocks - p.kv_blocks, turns);
+    if (block < p.kv_blocks) rotary_side<T, C, P, LANES, INTERLEAVED, STREAM, 1>(p, block, turns);
+    else if (block < 2 * p.kv_blocks) rotary_side<T, C, P, LANES, INTERLEAVED, STREAM, 2>(p, block - p.kv_blocks, turns);
+    else rotary_side<T, C, P, LANES, INTERLEAVED, STREAM, 0>(p, block - 2 * p.kv_blocks, turns);
 }
 
 // Any dims and pairs: 8 dims a lane, each of which finds its partner in LDS, where the row lies in fp32; the last
@@ -311,9 +312,9 @@ template <typename T, typename C, int LANES> __global__ __launch_bounds__(kMostT
     extern __shared__ __attribute__((aligned(16))) float2 turns[];
     __shared__ __attribute__((aligned(16))) float rows[kMostThreads * 8];
     const int block = (int)blockIdx.x;
-    if (block < p.q_blocks) rotary_side_any<T, C, LANES, 0>(p, block, rows, turns);
-    else if (block < p.q_blocks + p.kv_blocks) rotary_side_any<T, C, LANES, 1>(p, block - p.q_blocks, rows, turns);
-    else rotary_side_any<T, C, LANES, 2>(p, block - p.q_blocks - p.kv_blocks, rows, turns);
+    if (block < p.kv_blocks) rotary_side_any<T, C, LANES, 1>(p, block, rows, turns);
+    else if (block < 2 * p.kv_blocks) rotary_side_any<T, C, LANES, 2>(p, block - p.kv_blocks, rows, turns);
+    else rotary_side_any<T, C, LANES, 0>(p, block - 2 * p.kv_blocks, rows, turns);
 }
 
 // How a launch of teams of LANES lanes is divided.
@@ -342,6 +343,11 @@ Division divide(RotaryParams &q, int64_t tokens, int lanes) {
         if (busy > best + 0.02) best = busy, threads = n;
     }
     q.q_tokens = share(std::max(1, a.heads), threads), q.kv_tokens = share(std::max(1, a.kv_heads), threads);
+    // The scales of a page's tokens lie side by side for a head: into 8 bits a workgroup has twice as many of them
+    // (2048 tokens, 32 heads over 8, 10.2 -> 9.6 us, 32768 129 -> 128, dim 80 with 20 pairs 141 -> 133; four times
+    // 11.9, 125 and 129; values of 32 bits 270 and 272).
+    if (a.kv_heads && a.cache.dtype == CBS_DTYPE_I8 && a.dtype != CBS_DTYPE_F32)
+        q.kv_tokens = (int)std::min<int64_t>(most, 2 * q.kv_tokens);
     q.q_blocks = a.heads ? (int)((tokens + q.q_tokens - 1) / q.q_tokens) : 0;
     q.kv_blocks = a.kv_heads ? (int)((tokens + q.kv_tokens - 1) / q.kv_tokens) : 0;
     const int at_once = std::max(a.heads ? q.q_tokens : 0, a.kv_heads ? q.kv_tokens : 0);
