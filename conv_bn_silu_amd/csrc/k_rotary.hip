@@ -125,6 +125,9 @@ __device__ __forceinline__ void rotary_side(const RotaryParams &p, int block, fl
     const bool apart = !INTERLEAVED && lane < half;  // the second is not the one after the first
     const int d0 = apart ? P * lane : 2 * P * lane, d1 = apart ? d0 + pairs : d0 + P;
     const bool has0 = d0 < a.dim, has1 = d1 < a.dim;
+    // the lane's angles: two side by side, the next two `stride` further
+    const bool whole = !INTERLEAVED || pairs % P == 0;
+    const int first = whole ? 2 * lane : P * lane, stride = whole ? pairs / P * 2 : 2;
 
     Piece<T, P> next[2] = {};
     uint32_t next_slot = 0;
@@ -139,7 +142,7 @@ __device__ __forceinline__ void rotary_side(const RotaryParams &p, int block, fl
     if constexpr (SIDE != 2) {
         for (int i = (int)threadIdx.x; i < tokens * pairs; i += (int)blockDim.x) {
             const int t = (int)p.pairs.div((uint32_t)i), pair = i - t * pairs;
-            turns[t * pairs + (INTERLEAVED ? pair : turn_at<P>(pair, pairs))] = turn_of(a.rotary, a.positions[token0 + t], pair);
+            turns[t * pairs + (whole ? turn_at<P>(pair, pairs) : pair)] = turn_of(a.rotary, a.positions[token0 + t], pair);
         }
         __syncthreads();
     }
@@ -150,14 +153,14 @@ __device__ __forceinline__ void rotary_side(const RotaryParams &p, int block, fl
         if (i + teams < tasks) take(i + teams);
         const int t = (int)by_heads.div((uint32_t)i), h = i - t * heads;
         if (SIDE != 2 && turned) {
-            const float2 *const by = turns + t * pairs;
+            const float2 *const by = turns + t * pairs + first;
+            if (whole) {
 #pragma unroll
-            for (int e = 0; e < P; ++e) {
-                if constexpr (INTERLEAVED) {
-                    if (P * lane + e < pairs) turn(x[2 * e], x[2 * e + 1], by[P * lane + e]);
-                } else {
-                    turn(x[e], x[P + e], by[turn_at<P>(P * lane + e, pairs)]);
-                }
+                for (int e = 0; e < P; ++e) turn(x[INTERLEAVED ? 2 * e : e], x[INTERLEAVED ? 2 * e + 1 : P + e], by[e / 2 * stride + e % 2]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < P; ++e)
+                    if (P * lane + e < pairs) turn(x[2 * e], x[2 * e + 1], by[e]);
             }
         }
         if constexpr (SIDE == 0) {
