@@ -347,9 +347,9 @@ Division divide(RotaryParams &q, int64_t tokens, int lanes) {
     }
     q.q_tokens = share(std::max(1, a.heads), threads), q.kv_tokens = share(std::max(1, a.kv_heads), threads);
     // The scales of a page's tokens lie side by side for a head: into 8 bits a workgroup has twice as many of them
-    // (2048 tokens, 32 heads over 8, 10.2 -> 9.6 us, 32768 129 -> 128, dim 80 with 20 pairs 141 -> 133; four times
-    // 11.9, 125 and 129; values of 32 bits 270 and 272).
-    if (a.kv_heads && a.cache.dtype == CBS_DTYPE_I8 && a.dtype != CBS_DTYPE_F32)
+    // where that leaves one for every second CU (2048 tokens, 32 heads over 8, 10.2 -> 9.6 us, 32768 129 -> 128, dim 80
+    // with 20 pairs 141 -> 133; four times 11.9, 125 and 129; values of 32 bits 270 and 272).
+    if (a.kv_heads && a.cache.dtype == CBS_DTYPE_I8 && a.dtype != CBS_DTYPE_F32 && tokens >= 256 * (int64_t)q.kv_tokens)
         q.kv_tokens = (int)std::min<int64_t>(most, 2 * q.kv_tokens);
     q.q_blocks = a.heads ? (int)((tokens + q.q_tokens - 1) / q.q_tokens) : 0;
     q.kv_blocks = a.kv_heads ? (int)((tokens + q.kv_tokens - 1) / q.kv_tokens) : 0;
