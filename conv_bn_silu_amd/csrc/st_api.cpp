@@ -32,14 +32,21 @@ struct Heads {
     bool apart() const {
         return tokens <= 1 || heads <= 1 || token >= (heads - 1) * head + dim || head >= (tokens - 1) * token + dim;
     }
-    // Whether the two share no memory: they lie apart, or between each other's tokens.
+    // Whether the two share no memory: they lie apart, or between each other's tokens or heads.
     bool beside(const Heads &o) const {
         if (disjoint(all(), {o.all()})) return true;
-        if (token != o.token || e != o.e || tokens <= 1 || o.tokens <= 1) return false;
-        const int64_t period = token * e;
+        if (e != o.e) return false;
+        const bool tokens_alike = tokens > 1 && token == o.token, heads_alike = heads > 1 && head == o.head;
+        if (tokens_alike && between(o, token * e, extent(), o.extent())) return true;
+        if (heads_alike && between(o, head * e, ((tokens - 1) * token + dim) * e, ((o.tokens - 1) * o.token + o.dim) * e)) return true;
+        // every row begins at a multiple of the head stride from the first
+        return heads_alike && (tokens <= 1 || (tokens_alike && token % head == 0)) && between(o, head * e, dim * e, o.dim * e);
+    }
+    // Whether blocks of `mine` and `its` bytes, each repeated with this period, miss each other.
+    bool between(const Heads &o, int64_t period, int64_t mine, int64_t its) const {
         int64_t at = (int64_t)((uintptr_t)o.p - (uintptr_t)p) % period;
         if (at < 0) at += period;
-        return extent() <= at && at + o.extent() <= period;
+        return mine <= at && at + its <= period;
     }
 };
 

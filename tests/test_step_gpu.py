@@ -371,6 +371,31 @@ def test_rotary_cache_write(ops, shape, dtype, held):
         assert torch.equal(again.k.cpu()[pg, :, off], cache.k.cpu()[pg, :, off])
 
 
+@pytest.mark.parametrize("T", [1, 6])
+def test_rotary_cache_layouts(ops, T):
+    """Queries turned in their place beside the keys and values of their token, of their head, and head by head."""
+    H, D = 4, 64
+    g = gen(T)
+    q, k, v = (torch.randn(T, H, D, generator=g).to(BF16).cuda() for _ in range(3))
+    pos, slots, f = torch.arange(T, dtype=I32).cuda(), torch.arange(T, dtype=I32).cuda(), frequencies(32).cuda()
+    cache = ops.PagedCache.empty(2, H, 16, D)
+    want = ops.rotary_cache_write(cache, q, k, v, pos, slots, f)
+    for how in ("tokens", "heads", "three", "head major"):
+        if how == "tokens":
+            parts = torch.cat((q, k, v), 1).split(H, 1)
+        elif how == "heads":  # [tokens, heads, 3, dim]
+            parts = torch.stack((q, k, v), 2).unbind(2)
+        elif how == "three":  # [tokens, 3, heads, dim]
+            parts = torch.stack((q, k, v), 1).unbind(1)
+        else:  # [heads, 3, tokens, dim]
+            parts = [t.transpose(0, 1) for t in torch.stack([t.transpose(0, 1) for t in (q, k, v)], 1).unbind(1)]
+        again = ops.PagedCache.empty(2, H, 16, D)
+        got = ops.rotary_cache_write(again, *parts, pos, slots, f, out=parts[0])
+        assert got.data_ptr() == parts[0].data_ptr()
+        assert torch.equal(got, want) and torch.equal(parts[1], k) and torch.equal(parts[2], v), how
+        assert torch.equal(again.k, cache.k) and torch.equal(again.v, cache.v) and torch.equal(again.k_scale, cache.k_scale), how
+
+
 def test_rotary_cache_special_rows(ops):
     """Keys of zeros, infinities, NaN and of the smallest numbers; unaligned tensors."""
     T, H, D, P = 8, 2, 24, 4
