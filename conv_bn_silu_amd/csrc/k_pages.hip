@@ -10,7 +10,7 @@
 //
 // Bound by latency: a launch, the lengths, two sums over the workgroup, a page of the stack.  64 sequences with a
 // token each: 3.0 us on the GPU, and 2.7 to give them back (with the search for every token, and sums through LDS,
-// 6.8 and 4.0); the two calls take the host 8.  1024 prompts, 2.1 million tokens: 4 and 10 us, given back 3 and 3 (16 MB, which a
+// 6.8 and 4.0); the two calls take the host 7.5.  1024 prompts, 2.1 million tokens: 4 and 9 us, given back 3 and 3 (16 MB, which a
 // large copy would write in 3).
 #include <hip/hip_runtime.h>
 
@@ -24,8 +24,10 @@ namespace cbs {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-// Up to so many sequences, tokens and pages of the table one workgroup does it all; so many tokens or
-// pages of a sequence its thread does.
+// Up to so many sequences, tokens and entries of the table one workgroup does it all; so many tokens or
+// pages of a sequence its thread does.  How many pages come back is not known before: growing and giving back, us, by one
+// workgroup and by two launches, 64 sequences of 1001 entries: a page each 8.2 and 11.5, 20 pages 11.9 and 17.5, 1000 pages
+// 60 and 18.
 constexpr int kFewSequences = kThreads, kFewTokens = 2048, kFewEntries = 65536, kOwn = 8;
 constexpr uint32_t kManyTokens = 3u << 29;  // more than any batch has; twice that fits 32 bits
 
