@@ -72,8 +72,9 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = No
     * "turns": a pair that turns `high` times or more within the context stays, one that turns `low` times
       or less is divided by the factor, and between the two the frequency goes linearly with
       the number of turns;
-    * "pairs": the same with the share going linearly with the pair's number (between the pairs, rounded
-      outwards, that turn `high` and `low` times).
+    * "pairs": the same with the share going linearly with the pair's number, between the pairs that turn `high`
+      and `low` times: their numbers rounded outwards, the first 0 or more, the second dim - 1 or less.  The second
+      may lie past the last pair, dim / 2 - 1, which then keeps a share of its frequency.
     """
     if dim < 2 or dim % 2 or not base > 1 or not factor >= 1:
         raise ValueError("dim must be even and positive, base above 1, factor 1 or more")
@@ -93,7 +94,7 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = No
         else:
             def pair(turns):
                 return dim * math.log(context / (2 * math.pi * turns)) / (2 * math.log(base))
-            first, last = max(0, math.floor(pair(high))), min(dim // 2 - 1, math.ceil(pair(low)))
+            first, last = max(0, math.floor(pair(high))), min(dim - 1, math.ceil(pair(low)))
             share = 1 - ((i - first) / max(last - first, 1e-3)).clamp(0, 1)
         f = f * (share + (1 - share) / factor)
     elif scaling not in (None, "base"):

@@ -130,6 +130,27 @@ def test_frequencies():
             step.rotary_frequencies(**{**dict(dim=8, device="cpu"), **bad})
 
 
+@pytest.mark.parametrize("dim,context", [(8, 131072), (64, 131072), (128, 65536), (128, 131072), (128, 4096), (64, 300)])
+def test_frequencies_by_pairs_past_the_last_pair(dim, context):
+    """The share of each pair by the rule, one at a time; in long contexts the pair that turns `low` times is not there, and
+    the slowest keeps a share."""
+    low, high, factor, base = 1.0, 32.0, 4.0, 10000.0
+    got = step.rotary_frequencies(dim, base, "pairs", factor, context, low, high, device="cpu")
+
+    def number(turns):  # where base^(-2 i / dim) * context is that many whole turns
+        return math.log(context / (2 * math.pi * turns)) / math.log(base) * dim / 2
+
+    first, last = max(0, math.floor(number(high))), math.ceil(number(low))
+    assert last < dim
+    for i in range(dim // 2):
+        f = base ** (-2 * i / dim)
+        share = min(1.0, max(0.0, (last - i) / (last - first)))
+        assert math.isclose(float(got[i]), f * share + f / factor * (1 - share), rel_tol=1e-12), i
+    slowest = base ** (2 / dim - 1)
+    if context * slowest > 2 * math.pi * low:
+        assert last > dim // 2 - 1 and float(got[-1]) > 1.05 * slowest / factor
+
+
 def test_oracle_norm_and_rotation():
     """Hand-checked: rows of 3 and 4; quarter turns."""
     y, _, h = S.norm(torch.tensor([[1.0, 5.0]]), torch.tensor([2.0, 1.0]), torch.tensor([[2.0, -1.0]]), 0.0)
