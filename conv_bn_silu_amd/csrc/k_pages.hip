@@ -245,7 +245,7 @@ __global__ __launch_bounds__(kThreads) void release(const PagesParams p) {
         for (int b0 = 0; b0 < a.batch; b0 += threads) {
             const int b = b0 + tid;
             const bool mine = b < a.batch;
-            const int len = mine ? max(0, a.lens[b]) : 0, keep = mine ? min(len, max(0, a.change[b])) : 0;
+            const int held = mine ? a.lens[b] : 0, len = max(0, held), keep = mine ? min(len, max(0, a.change[b])) : 0;
             const int first = pages_for(p.page, keep);
             const int last = (int)min((int64_t)pages_for(p.page, len), a.table_width);
             const int n = max(0, last - first);
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(kThreads) void release(const PagesParams p) {
             if (pass == 1 && mine) {
                 const int64_t top = (int64_t)count + total - 1 - upto;
                 r = Released{first, n, (int)min(top, (int64_t)INT32_MAX), 0};
-                if (keep < len) a.lens[b] = keep;
+                if (keep != held) a.lens[b] = keep;
                 if (!p.whole) ((Released *)a.workspace)[b] = r;
             }
             if (a.batch > threads) __syncthreads();  // part is free again

@@ -99,8 +99,7 @@ class Pages:
             for i in range(-(-k // p), min(-(-l // p), len(self.table[b]))):
                 back.append(self.table[b][i])
                 self.table[b][i] = -1
-            if k < l:
-                self.lens[b] = k
+            self.lens[b] = k
         for r, page in enumerate(back):
             to = self.count + len(back) - 1 - r
             if to < len(self.below):
