@@ -30,6 +30,7 @@ constexpr int kThreads = 1024, kWaves = kThreads / 64;
 // 60 and 18.
 constexpr int kFewSequences = kThreads, kFewTokens = 2048, kFewEntries = 65536, kOwn = 8;
 constexpr uint32_t kManyTokens = 3u << 29;  // more than any batch has; twice that fits 32 bits
+constexpr uint32_t kManyPages = INT32_MAX;  // as many as a pool may have; twice that fits, too
 
 struct Grown {
     int len;    // tokens before, -1 where the sequence is left as it is
@@ -250,8 +251,8 @@ __global__ __launch_bounds__(kThreads) void release(const PagesParams p) {
             const int last = (int)min((int64_t)pages_for(p.page, len), a.table_width);
             const int n = max(0, last - first);
             uint32_t all;
-            const uint32_t upto = before + sum_before((uint32_t)n, kManyTokens, part, all);
-            before = min(before + all, kManyTokens);
+            const uint32_t upto = before + sum_before((uint32_t)n, kManyPages, part, all);
+            before = min(before + all, kManyPages);
             if (a.batch <= threads) total = all;
             if (pass == 1 && mine) {
                 const int64_t top = (int64_t)count + total - 1 - upto;

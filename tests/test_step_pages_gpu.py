@@ -37,3 +37,24 @@ def test_release_of_negative_lengths(ops, n, width):
     ops.release_pages(pool, table, lens, i32(keep))
     assert lens.tolist() == [min(max(0, w), max(0, k)) for w, k in zip(was, keep)]
     assert pool.report()[0] == 2 * n + sum([1, 0, 0, 0, 2][b % 5] for b in range(n))
+
+
+@pytest.mark.parametrize("batch", [1024, 65536])
+def test_release_of_as_many_pages_as_a_pool_may_have(ops, batch):
+    """1.8 billion pages of one token come back at once, the first on top."""
+    width, spare = 1_800_000_000 // batch, 12345
+    n = batch * width
+    say("[most pages]", batch, n)
+    table = torch.arange(n, dtype=I32, device="cuda").view(batch, width)
+    free = torch.full((n + spare,), -5, dtype=I32, device="cuda")
+    free[:spare] = torch.arange(n, n + spare, dtype=I32, device="cuda")
+    pool = ops.PagePool(free, i32([spare, 0, 0]), 1)
+    lens = torch.full((batch,), width, dtype=I32, device="cuda")
+    ops.release_pages(pool, table, lens, torch.zeros_like(lens))
+    assert pool.report()[0] == n + spare
+    assert bool((table == -1).all()) and not bool(lens.any())
+    del table
+    assert torch.equal(free[:spare], torch.arange(n, n + spare, dtype=I32, device="cuda"))
+    assert torch.equal(free[spare:], torch.arange(n - 1, -1, -1, dtype=I32, device="cuda"))
+    del free, pool
+    torch.cuda.empty_cache()
