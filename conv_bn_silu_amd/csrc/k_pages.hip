@@ -6,11 +6,11 @@
 // its tokens need to know.  Where no sequence has more than a few new tokens, as in a decoding step, its
 // thread goes on to write their slots and positions itself; else the tokens find their sequences by
 // bisection, in the same workgroup where they are few, in a second kernel (place) where they are many.  Giving back
-// is the same the other way round (release, move_back).
+// is the same the other way round (release; count_back and move_back).
 //
 // Bound by latency: a launch, the lengths, two sums over the workgroup, a page of the stack.  64 sequences with a
 // token each: 3.0 us on the GPU, and 2.7 to give them back (with the search for every token, and sums through LDS,
-// 6.8 and 4.0); the two calls take the host 7.5.  1024 prompts, 2.1 million tokens: 4 and 9 us, given back 3 and 3 (16 MB, which a
+// 6.8 and 4.0); the two calls take the host 7.5.  1024 prompts, 2.1 million tokens: 4 and 9 us, given back 6.6 (16 MB, which a
 // large copy would write in 3).
 #include <hip/hip_runtime.h>
 
@@ -25,10 +25,11 @@ namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 // Up to so many sequences, tokens and entries of the table one workgroup does it all; so many tokens or
-// pages of a sequence its thread does.  How many pages come back is not known before: growing and giving back, us, by one
-// workgroup and by two launches, 64 sequences of 1001 entries: a page each 8.2 and 11.5, 20 pages 11.9 and 17.5, 1000 pages
-// 60 and 18.
+// pages of a sequence its thread does.  How many pages come back is not known before: giving back, us on the GPU, by one
+// workgroup and by two launches (64 and 66 sequences of 1000 entries): a page each 2.7 and 5.0, 20 pages 4.6 and 5.2,
+// 1000 pages 57 and 7.3.
 constexpr int kFewSequences = kThreads, kFewTokens = 2048, kFewEntries = 65536, kOwn = 8;
+constexpr int kFewItems = 4096;  // of release, that every workgroup sums by itself
 constexpr uint32_t kManyTokens = 3u << 29;  // more than any batch has; twice that fits 32 bits
 constexpr uint32_t kManyPages = INT32_MAX;  // as many as a pool may have; twice that fits, too
 
@@ -38,16 +39,11 @@ struct Grown {
     int top;    // of the stack: its first new page's place
     int start;  // of its tokens in the batch
 };
-struct Released {
-    int first, count;  // entries of its row
-    int top;           // of the stack: the first's place
-    int pad;
-};
 
 struct PagesParams {
     PagesArgs a;
     FastDiv page;
-    bool whole;  // the one workgroup also writes slots, or moves pages
+    bool whole;  // the one workgroup also writes slots
 };
 
 // Sums of `v` over the workgroup's threads before this one, which do not pass `most` (below 2^31); `all` gets that of
@@ -220,88 +216,201 @@ __global__ __launch_bounds__(256) void place(const PagesParams p) {
     if (t < a.tokens) place_tokens<4>(p, t, a.starts, (const Grown *)a.workspace, sequence_of(a.starts, t, ends[0], ends[1]));
 }
 
-// Entries [from, from + step, ...) of a sequence's pages that go back.
-__device__ __forceinline__ void give_back(const PagesArgs &a, int b, const Released &r, int from, int step) {
-    int32_t *const row = a.table + (int64_t)b * a.table_stride + r.first;
-    for (int i = from; i < r.count; i += step) {
-        const int page = row[i], to = r.top - i;
-        if (to >= 0 && to < a.pool.pages) a.pool.free[to] = page;
-        row[i] = -1;
-    }
+// Giving back.  Only entries that name pages of the pool go to the stack: in a row there may be holes (pages
+// that a window has left behind).  So an entry's place is the number of such entries after it, above what the stack
+// holds, and the sums run from the last entry to the first.
+__device__ __forceinline__ bool in_pool(const PagesArgs &a, int page) { return page >= 0 && page < a.pool.pages; }
+__device__ __forceinline__ void push(const PagesArgs &a, int64_t to, int page) {
+    if (to < a.pool.pages) a.pool.free[to] = page;
+}
+struct Cut {
+    int held, keep;    // tokens as the lengths have them, and that stay
+    int first, count;  // entries of its row that go
+};
+__device__ __forceinline__ Cut cut_of(const PagesParams &p, int b) {
+    const int held = p.a.lens[b], len = max(0, held), keep = min(len, max(0, p.a.change[b])), first = pages_for(p.page, keep);
+    return Cut{held, keep, first, max(0, (int)min((int64_t)pages_for(p.page, len), p.a.table_width) - first)};
 }
 
+// All of it by one workgroup, a sequence a thread.
 __global__ __launch_bounds__(kThreads) void release(const PagesParams p) {
-    __shared__ uint32_t part[kWaves];
-    __shared__ Released few[kFewSequences];
-    __shared__ int32_t few_begin[kFewSequences];  // pages that those before give back
+    __shared__ uint32_t part[kWaves], of_64[2][4 * kWaves];
+    __shared__ int few_first[kFewSequences];
+    __shared__ int32_t few_begin[kFewSequences];  // entries of those before
     const PagesArgs &a = p.a;
     const int tid = (int)threadIdx.x, threads = (int)blockDim.x;
     const int count = max(0, min(a.pool.counts[0], (int)a.pool.pages));
-    uint32_t total = 0;
-    Released r{0, 0, 0, 0};
-    // The first page given back lies on top of all, so that their number comes first: twice through the
-    // sequences, or once where each has a thread.
-    for (int pass = a.batch <= threads ? 1 : 0; pass < 2; ++pass) {
-        uint32_t before = 0;
-        for (int b0 = 0; b0 < a.batch; b0 += threads) {
-            const int b = b0 + tid;
-            const bool mine = b < a.batch;
-            const int held = mine ? a.lens[b] : 0, len = max(0, held), keep = mine ? min(len, max(0, a.change[b])) : 0;
-            const int first = pages_for(p.page, keep);
-            const int last = (int)min((int64_t)pages_for(p.page, len), a.table_width);
-            const int n = max(0, last - first);
-            uint32_t all;
-            const uint32_t upto = before + sum_before((uint32_t)n, kManyPages, part, all);
-            before = min(before + all, kManyPages);
-            if (a.batch <= threads) total = all;
-            if (pass == 1 && mine) {
-                const int64_t top = (int64_t)count + total - 1 - upto;
-                r = Released{first, n, (int)min(top, (int64_t)INT32_MAX), 0};
-                if (keep != held) a.lens[b] = keep;
-                if (!p.whole) ((Released *)a.workspace)[b] = r;
-            }
-            if (a.batch > threads) __syncthreads();  // part is free again
+    const bool mine = tid < a.batch;
+    const Cut c = mine ? cut_of(p, tid) : Cut{0, 0, 0, 0};
+    int32_t *const row = a.table + (int64_t)tid * a.table_stride + c.first;
+    if (c.keep != c.held) a.lens[tid] = c.keep;
+    // its own entries, if they are few, on their way
+    int page[kOwn];
+    uint32_t there = 0;  // a bit for each page of the pool
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) page[i] = i < c.count ? row[i] : -1;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) there |= in_pool(a, page[i]) ? 1u << i : 0;
+    uint32_t all;
+    int64_t base = count;
+    if (!__syncthreads_or(c.count > kOwn)) {  // and everyone has read the count
+        const uint32_t before = sum_before((uint32_t)__builtin_popcount(there), kManyPages, part, all);
+        int64_t to = base + all - 1 - before;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            if (i >= c.count) break;
+            if (there >> i & 1) push(a, to--, page[i]);
+            row[i] = -1;
         }
-        total = before;
-    }
-    if (!__syncthreads_or(p.whole && r.count > kOwn)) {  // and everyone has read the count
-        if (p.whole && r.count > 0) give_back(a, tid, r, 0, 1);
+        base += all;
     } else {
-        // pages over the threads, four on their way at a time
-        few[tid] = r;
-        few_begin[tid] = count + (int)total - 1 - r.top;
+        // entries over the threads, from the last, four on their way at a time: of each 64 those of the pool are
+        // counted, and the counts summed by every wave
+        uint32_t entries;
+        const uint32_t begin = sum_before((uint32_t)c.count, kManyPages, part, entries);
+        few_first[tid] = c.first, few_begin[tid] = (int)begin;
         __syncthreads();
-        for (int e0 = tid; e0 < (int)total; e0 += 4 * threads) {
+        const int lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), waves = threads / 64;
+        int turn = 0;
+        for (int e0 = (int)entries - 1 - tid; e0 + tid >= 0; e0 -= 4 * threads, turn ^= 1) {
             int32_t *entry[4];
-            int page[4], to[4];
+            int page[4];
+            uint64_t those[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int e = e0 + u * threads;
-                if (e >= (int)total) continue;
-                const int b = sequence_of(few_begin, e, 0, a.batch - 1), i = e - few_begin[b];
-                entry[u] = a.table + (int64_t)b * a.table_stride + few[b].first + i;
-                page[u] = *entry[u], to[u] = few[b].top - i;
+                const int e = e0 - u * threads;
+                page[u] = -1;
+                if (e < 0) continue;
+                const int b = sequence_of(few_begin, e, 0, a.batch - 1);
+                entry[u] = a.table + (int64_t)b * a.table_stride + few_first[b] + (e - few_begin[b]);
+                page[u] = *entry[u];
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (e0 + u * threads >= (int)total) continue;
-                if (to[u] >= 0 && to[u] < a.pool.pages) a.pool.free[to[u]] = page[u];
-                *entry[u] = -1;
+                those[u] = __ballot(in_pool(a, page[u]));
+                if (lane == 0) of_64[turn][u * kWaves + wave] = (uint32_t)__builtin_popcountll(those[u]);
             }
+            __syncthreads();
+            const uint32_t upto = lanes_upto(lane % kWaves < waves ? of_64[turn][lane] : 0, kManyPages);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int its = u * kWaves + wave;
+                const uint32_t before = its ? (uint32_t)__builtin_amdgcn_readlane((int)upto, its - 1) : 0;
+                if (those[u] >> lane & 1) push(a, base + before + __builtin_popcountll(those[u] & ((1ull << lane) - 1)), page[u]);
+                if (e0 - u * threads >= 0) *entry[u] = -1;
+            }
+            base += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
         }
     }
-    if (tid == 0) a.pool.counts[0] = (int)min((int64_t)count + total, a.pool.pages);
+    if (tid == 0) a.pool.counts[0] = (int)min(base, a.pool.pages);
 }
 
-// A part of a sequence's pages to a workgroup: blockIdx.x the sequence, blockIdx.y the part.
-__global__ __launch_bounds__(256) void move_back(const PagesParams p) {
-    const int b = (int)blockIdx.x;
-    const Released r = ((const Released *)p.a.workspace)[b];
-    give_back(p.a, b, r, (int)blockIdx.y * 256 + (int)threadIdx.x, (int)gridDim.y * 256);
+// Where one workgroup would take long: items, each a part of a sequence's entries; `parts` of them to a sequence, in
+// the order of the entries.  count_back notes what each has, move_back moves it.
+struct Back {
+    int first, count;  // entries of the row
+    int there;         // of them pages of the pool
+    int after;         // such entries of all items after it; where there are many, by sum_back
+};
+struct BackPlan {
+    Back *items;
+    int32_t *there, *count;  // the items' once more, side by side; the stack's before
+    int n, parts;
+};
+
+// An item to a wave.
+__global__ __launch_bounds__(64) void count_back(const PagesParams p, const BackPlan plan) {
+    const PagesArgs &a = p.a;
+    const int lane = (int)threadIdx.x, i = (int)blockIdx.x, b = i / plan.parts;
+    const Cut c = cut_of(p, b);
+    const int64_t share = ((int64_t)c.count + plan.parts - 1) / plan.parts, from = min(share * (i - b * plan.parts), (int64_t)c.count);
+    const int first = c.first + (int)from, n = (int)min(share, c.count - from);
+    const int32_t *const row = a.table + (int64_t)b * a.table_stride + first;
+    uint32_t there = 0;
+    for (int64_t e0 = 0; e0 < n; e0 += 256) {
+        int page[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) page[u] = e0 + u * 64 + lane < n ? row[e0 + u * 64 + lane] : -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) there += in_pool(a, page[u]);
+    }
+    there = team_sum_of<64>(there);
+    if (lane != 0) return;
+    plan.items[i] = Back{first, n, (int)there, 0};
+    plan.there[i] = (int)there;
+    if (i == 0) *plan.count = max(0, min(a.pool.counts[0], (int)a.pool.pages));
+}
+
+// Where there are more items than a workgroup of move_back sums by itself.
+__global__ __launch_bounds__(kThreads) void sum_back(const BackPlan plan) {
+    __shared__ uint32_t part[2][kWaves];
+    uint32_t after = 0, all;
+    int turn = 0;
+    for (int i0 = plan.n - 1; i0 >= 0; i0 -= kThreads, turn ^= 1) {
+        const int i = i0 - (int)threadIdx.x;
+        const uint32_t before = sum_before(i >= 0 ? (uint32_t)plan.there[i] : 0, kManyPages, part[turn], all);
+        if (i >= 0) plan.items[i].after = (int)min(after + before, kManyPages);
+        after = min(after + all, kManyPages);
+    }
+}
+
+__global__ __launch_bounds__(256) void move_back(const PagesParams p, const BackPlan plan) {
+    __shared__ double sums[4];
+    __shared__ int part[2][4];
+    const PagesArgs &a = p.a;
+    const int tid = (int)threadIdx.x, lane = tid % 64, wave = tid / 64, i = (int)blockIdx.x, b = i / plan.parts;
+    const Back r = plan.items[i];
+    int32_t *const row = a.table + (int64_t)b * a.table_stride + r.first;
+    int next = tid < r.count ? row[r.count - 1 - tid] : -1;  // on its way while the others' are summed
+    if (tid == 0 && i == b * plan.parts) {
+        const Cut c = cut_of(p, b);  // no other workgroup reads the lengths any more
+        if (c.keep != c.held) a.lens[b] = c.keep;
+    }
+    if (r.count == 0 && i != 0) return;
+    int64_t base = *plan.count;
+    if (plan.n <= kFewItems) {
+        double after = 0;  // whole numbers below 2^53
+        for (int j = i + 1 + tid; j < plan.n; j += 256) after += plan.there[j];
+        after = team_sum<64>(after);
+        if (lane == 0) sums[wave] = after;
+        __syncthreads();
+        base += (int64_t)(sums[0] + sums[1] + sums[2] + sums[3]);
+    } else {
+        base += r.after;
+    }
+    if (tid == 0 && i == 0) a.pool.counts[0] = (int)min(base + r.there, a.pool.pages);
+    const bool holes = r.there != r.count;
+    int turn = 0;
+    for (int64_t e = (int64_t)r.count - 1 - tid; e + tid >= 0; e -= 256, turn ^= 1) {
+        const int page = next;
+        if (e >= 256) next = row[e - 256];
+        bool there = e >= 0;
+        int before = tid, all = 256;
+        if (holes) {
+            there = there && in_pool(a, page);
+            const uint64_t those = __ballot(there);
+            if (lane == 0) part[turn][wave] = __builtin_popcountll(those);
+            __syncthreads();
+            before = __builtin_popcountll(those & ((1ull << lane) - 1)), all = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (w < wave) before += part[turn][w];
+                all += part[turn][w];
+            }
+        }
+        if (there) push(a, base + before, page);
+        if (e >= 0) row[e] = -1;
+        base += all;
+    }
 }
 
 bool grows_whole(int64_t batch, int64_t tokens) { return batch <= kFewSequences && tokens <= kFewTokens; }
 bool releases_whole(int64_t batch, int64_t width) { return batch <= kFewSequences && batch * width <= kFewEntries; }
+// Items to a sequence: each has the better part of 1024 entries or more, and a few sequences make no more items than
+// move_back sums.
+int64_t parts_of(int64_t batch, int64_t width) {
+    return std::max<int64_t>(1, std::min<int64_t>((width + 1023) / 1024, kFewItems / batch));
+}
 // Whole waves for n sequences or tokens.
 int threads_for(int64_t n) { return (int)std::min<int64_t>(kThreads, std::max<int64_t>(64, (n + 63) / 64 * 64)); }
 
@@ -309,7 +418,7 @@ int threads_for(int64_t n) { return (int)std::min<int64_t>(kThreads, std::max<in
 
 int64_t grow_workspace(int64_t batch, int64_t tokens) { return grows_whole(batch, tokens) ? 0 : batch * (int64_t)sizeof(Grown); }
 int64_t release_workspace(int64_t batch, int64_t width) {
-    return releases_whole(batch, width) ? 0 : batch * (int64_t)sizeof(Released);
+    return releases_whole(batch, width) ? 0 : batch * parts_of(batch, width) * (int64_t)(sizeof(Back) + 4) + 4;
 }
 
 hipError_t launch_grow_pages(const PagesArgs &a, hipStream_t st) {
@@ -320,12 +429,19 @@ hipError_t launch_grow_pages(const PagesArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_release_pages(const PagesArgs &a, hipStream_t st) {
-    const PagesParams p{a, make_fastdiv((uint32_t)a.pool.page_size), releases_whole(a.batch, a.table_width)};
-    release<<<1, threads_for(p.whole ? std::max<int64_t>(a.batch, a.batch * a.table_width / 16) : a.batch), 0, st>>>(p);
-    if (!p.whole) {
-        const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((a.table_width + 1023) / 1024, 16384 / a.batch));
-        move_back<<<dim3((unsigned)a.batch, (unsigned)parts), 256, 0, st>>>(p);
+    const bool whole = releases_whole(a.batch, a.table_width);
+    const PagesParams p{a, make_fastdiv((uint32_t)a.pool.page_size), whole};
+    if (whole) {
+        release<<<1, threads_for(std::max<int64_t>(a.batch, a.batch * a.table_width / 16)), 0, st>>>(p);
+        return hipGetLastError();
     }
+    const int parts = (int)parts_of(a.batch, a.table_width), n = a.batch * parts;
+    Back *const items = (Back *)a.workspace;
+    int32_t *const there = (int32_t *)(items + n);
+    const BackPlan plan{items, there, there + n, n, parts};
+    count_back<<<(unsigned)n, 64, 0, st>>>(p, plan);
+    if (n > kFewItems) sum_back<<<1, kThreads, 0, st>>>(plan);
+    move_back<<<(unsigned)n, 256, 0, st>>>(p, plan);
     return hipGetLastError();
 }
 

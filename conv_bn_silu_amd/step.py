@@ -178,7 +178,8 @@ def grow_pages(pool: PagePool, table, lens, more, tokens: int, library: Library 
 
 def release_pages(pool: PagePool, table, lens, keep, library: Library | None = None):
     """Sequences keep their first keep[b] tokens (0 where they have ended, fewer where drafts were rejected);
-    the other pages go back to the pool, their entries of the table become -1, and lens is updated.
+    the other pages go back to the pool, their entries of the table become -1, and lens is updated.  Entries that name
+    no page of the pool (-1 where a page has been given back before, say) give nothing back.
 
     What ``grow_pages`` took and is given back at once lies in the pool as it did before.
     """

@@ -110,7 +110,8 @@ int64_t cbs_grow_pages_workspace(int64_t batch, int64_t tokens);
 
 /* The sequences keep their first keep[b] tokens (all, where they have no more): lens[b] becomes the smaller
  * of the two (negative ones count as 0), the pages past those tokens go back to the pool and their entries of
- * the table become -1.  Of all pages given back, in the order of the sequences and of their rows, the first
+ * the table become -1.  An entry that names no page of the pool (a hole that a window has left behind) gives
+ * nothing back.  Of all pages given back, in the order of the sequences and of their rows, the first
  * ends on top of the stack: what cbs_grow_pages took and is given back at once lies as it did before.  What
  * does not fit the stack is dropped (then some page was in it twice).
  *   keep: int32 [batch].  Sizes as above; table_width < 2^31.

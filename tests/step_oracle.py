@@ -100,6 +100,7 @@ class Pages:
                 back.append(self.table[b][i])
                 self.table[b][i] = -1
             self.lens[b] = k
+        back = [page for page in back if 0 <= page < len(self.below)]
         for r, page in enumerate(back):
             to = self.count + len(back) - 1 - r
             if to < len(self.below):

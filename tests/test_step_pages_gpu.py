@@ -58,3 +58,72 @@ def test_release_of_as_many_pages_as_a_pool_may_have(ops, batch):
     assert torch.equal(free[spare:], torch.arange(n - 1, -1, -1, dtype=I32, device="cuda"))
     del free, pool
     torch.cuda.empty_cache()
+
+
+def given_back(table, lens, keep, page, free, count):
+    """The rule: pages past the tokens that stay, of those that the pool has, the first on top."""
+    table, free, back = [list(r) for r in table], list(free), []
+    for b, row in enumerate(table):
+        has = max(lens[b], 0)
+        stays = min(has, max(keep[b], 0))
+        for i in range(-(-stays // page), min(-(-has // page), len(row))):
+            if 0 <= row[i] < len(free):
+                back.append(row[i])
+            row[i] = -1
+    stack = (free[:count] + back[::-1])[:len(free)]
+    return table, stack + free[len(stack):], len(stack)
+
+
+HOLES = [
+    # sequences, width, pages of each that come back: by threads, by one workgroup, by parts of rows, by several launches
+    (1, 5, 5), (9, 8, 6), (1000, 60, 8), (9, 300, 300), (700, 90, 70), (64, 1000, 900), (1, 40000, 30000), (3, 30000, 27001),
+    (1100, 40, 7), (1500, 60, 50), (5000, 30, 23),
+]
+
+
+@pytest.mark.parametrize("share", [0.0, 0.3, 1.0], ids=["whole", "some", "all"])
+@pytest.mark.parametrize("shape", HOLES, ids=lambda s: "x".join(map(str, s)))
+def test_release_of_rows_with_holes(ops, shape, share):
+    """Entries that name no page of the pool give nothing back; what grows next gets pages only."""
+    n, width, per = shape
+    say("[holes]", shape, share)
+    page, g = 3, torch.Generator().manual_seed(n + width)
+    was = [per - b % 3 if per > 3 else per for b in range(n)]
+    pages = sum(was) + 50
+    order = torch.randperm(pages, generator=g)
+    table, at = torch.full((n, width), -1, dtype=I32), 0
+    for b, w in enumerate(was):
+        table[b, :w] = order[at:at + w]
+        at += w
+    holes = torch.rand(n, width, generator=g) < share
+    table = torch.where(holes, torch.tensor([-1, -1, pages, 2 ** 31 - 1, -2 ** 31], dtype=I32)[torch.arange(width) % 5], table)
+    lens = [max(0, w * page - b % page) for b, w in enumerate(was)]
+    keep = [[0, 4, 10, 2 ** 31 - 1, 0][b % 5] for b in range(n)]
+    # what a window has left behind is in the stack already: with the holes it would not fit
+    left = order[torch.isin(order, table[table >= 0], invert=True)].tolist()
+    free = left + [-9] * (pages - len(left))
+    want, stack, count = given_back(table.tolist(), lens, keep, page, free, len(left))
+    pool = ops.PagePool(i32(free), i32([len(left), 0, 0]), page)
+    on, dlens = table.cuda(), i32(lens)
+    ops.release_pages(pool, on, dlens, i32(keep))
+    assert pool.report()[0] == count and torch.equal(on.cpu(), torch.tensor(want, dtype=I32))
+    assert torch.equal(pool.free.cpu(), torch.tensor(stack, dtype=I32))
+    assert dlens.tolist() == [min(a, b) for a, b in zip(lens, keep)]
+    # all that the pool has goes to new sequences, and every one of their tokens has a slot
+    new = torch.full((1, count), -1, dtype=I32, device="cuda")
+    _, slots, _ = ops.grow_pages(pool, new, i32([0]), i32([count * page]), count * page)
+    assert pool.report() == (0, 0, 0) and new[0].tolist() == stack[:count][::-1]
+    assert int(slots.min()) >= 0 and int(slots.unique().numel()) == count * page
+
+
+def test_release_of_more_than_the_stack_holds(ops):
+    """Pages that are in the table twice: the first given back, which would lie past the stack, are dropped."""
+    for n, width in ((2, 6), (2, 40000), (6000, 12)):
+        say("[twice]", n, width)
+        table = (torch.arange(n * width, dtype=I32) % (n * width // 2)).view(n, width)
+        lens, keep, free = [width] * n, [0] * n, [7] * (n * width // 2)
+        want, stack, count = given_back(table.tolist(), lens, keep, 1, free, 5)
+        pool, on, dlens = ops.PagePool(i32(free), i32([5, 0, 0]), 1), table.cuda(), i32(lens)
+        ops.release_pages(pool, on, dlens, i32(keep))
+        assert pool.report()[0] == count == len(free) and torch.equal(pool.free.cpu(), torch.tensor(stack, dtype=I32))
+        assert bool((on == -1).all()) and not bool(dlens.any())
