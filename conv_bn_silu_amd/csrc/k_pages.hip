@@ -83,21 +83,26 @@ __device__ __forceinline__ int sequence_of(const int32_t *starts, int t, int lo,
 }
 
 // Tokens [t, t + N) of the batch: their slots and positions, and the entries of new pages that begin with
-// them.  Sequence b is the last that begins at t or before it.
+// them.  Sequence b is the last that begins at t or before it, and none beyond `last` begins within them.
 template <int N>
-__device__ __forceinline__ void place_tokens(const PagesParams &p, int t, const int32_t *starts, const Grown *grown, int b) {
+__device__ __forceinline__ void place_tokens(const PagesParams &p, int t, const int32_t *starts, const Grown *grown, int b, int last) {
     const PagesArgs &a = p.a;
     int slot[N], pos[N], page = -1, page_b = -1, page_no = -1;
     Grown g{-1, 0, 0, 0};
-    int next = t, had = -1;  // where b ends, and the sequence that g is of
+    int next = b < a.batch ? starts[b + 1] : t, had = -1;  // where b ends, and the sequence that g is of
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         slot[i] = -1, pos[i] = 0;
-        while (b < a.batch && t + i >= next) {
-            next = starts[b + 1];
-            if (t + i >= next) ++b;
+        if (t + i >= a.tokens) continue;
+        if (b < a.batch && t + i >= next) {
+            // the next one, or behind a run of idle ones
+            if (++b < a.batch) next = starts[b + 1];
+            if (b < a.batch && t + i >= next) {
+                b = sequence_of(starts, t + i, b + 1, last);
+                if (b < a.batch) next = starts[b + 1];
+            }
         }
-        if (b >= a.batch || t + i >= a.tokens) continue;
+        if (b >= a.batch) continue;
         if (had != b) g = grown[b], had = b;
         if (g.len < 0) continue;
         pos[i] = g.len + (t + i - g.start);
@@ -190,7 +195,7 @@ __global__ __launch_bounds__(kThreads) void grow(const PagesParams p) {
     if (tid < a.batch) few[tid] = g, few_starts[tid] = start;
     if (tid == 0) few_starts[a.batch] = tokens_end;
     __syncthreads();
-    for (int t = tid; t < a.tokens; t += threads) place_tokens<1>(p, t, few_starts, few, sequence_of(few_starts, t, 0, a.batch));
+    for (int t = tid; t < a.tokens; t += threads) place_tokens<1>(p, t, few_starts, few, sequence_of(few_starts, t, 0, a.batch), a.batch);
 }
 
 // 1024 tokens to a workgroup of 256.  Its first two waves look for the sequences of the first and the last of
@@ -213,7 +218,7 @@ __global__ __launch_bounds__(256) void place(const PagesParams p) {
     }
     __syncthreads();
     const int t = t0 + (int)threadIdx.x * 4;
-    if (t < a.tokens) place_tokens<4>(p, t, a.starts, (const Grown *)a.workspace, sequence_of(a.starts, t, ends[0], ends[1]));
+    if (t < a.tokens) place_tokens<4>(p, t, a.starts, (const Grown *)a.workspace, sequence_of(a.starts, t, ends[0], ends[1]), ends[1]);
 }
 
 // Giving back.  Only entries that name pages of the pool go to the stack: in a row there may be holes (pages

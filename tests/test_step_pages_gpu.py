@@ -127,3 +127,34 @@ def test_release_of_more_than_the_stack_holds(ops):
         ops.release_pages(pool, on, dlens, i32(keep))
         assert pool.report()[0] == count == len(free) and torch.equal(pool.free.cpu(), torch.tensor(stack, dtype=I32))
         assert bool((on == -1).all()) and not bool(dlens.any())
+
+
+def test_growth_past_runs_of_idle_sequences(ops):
+    """Tokens find their sequences past tens of thousands that bring none, and no slower for where those lie: walked one
+    by one, the run costs thousands of times the search."""
+    n, per, page = 65536, 1501, 16
+    at = [5, 30000, 30002, 65535]
+    times = []
+    for where in (at, [0, 1, 2, 3]):
+        more = torch.zeros(n, dtype=I32)
+        more[where] = per
+        say("[idle]", where)
+        pool = ops.PagePool.full(4 * 95, page)
+        table, lens = torch.full((n, 95), -1, dtype=I32, device="cuda"), torch.zeros(n, dtype=I32, device="cuda")
+        more, keep, tokens = more.cuda(), torch.zeros_like(lens), 4 * per + 70
+        for turn in range(5):
+            ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            ev[0].record()
+            starts, slots, positions = ops.grow_pages(pool, table, lens, more, tokens)
+            ev[1].record()
+            torch.cuda.synchronize()
+            times.append(ev[0].elapsed_time(ev[1]))
+            i = torch.arange(4 * per, dtype=I32)
+            # a full pool hands out pages 0, 1, ... in order
+            assert pool.report() == (4, 0, 0) and torch.equal(positions[:4 * per].cpu(), i % per)
+            assert torch.equal(slots[:4 * per].cpu(), i // per * 94 * page + i % per)
+            assert bool((slots[4 * per:] == -1).all()) and bool((positions[4 * per:] == 0).all())
+            assert torch.equal(lens, more) and torch.equal(starts[1:].cpu().long(), more.cpu().long().cumsum(0))
+            ops.release_pages(pool, table, lens, keep)
+    print("idle between %.3f ms, behind %.3f ms" % (min(times[:5]), min(times[5:])))
+    assert min(times[:5]) < 20 * min(times[5:])
