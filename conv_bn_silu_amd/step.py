@@ -172,6 +172,10 @@ def grow_pages(pool: PagePool, table, lens, more, tokens: int, library: Library 
     ``paged_attention`` take.  Sequences grow in order as long as there are pages; the first that lacks
     some, and all after it, are left as they are, as is one that would pass its row of the table or whose tokens pass
     `tokens`.  Tokens without a place (and padding) have slot -1 and position 0.  ``pool.report()`` says how it went.
+
+    ``paged_attention`` goes by lens and does not look at slots: it takes the rows of a sequence that was left for its
+    last old tokens, so that its output there stands for no token.  Where a step may be short of pages, use rows with
+    ``slots >= 0`` only (``masked_fill_`` by ``slots < 0`` does it without the host), and bring the other tokens again.
     """
     return _checked(_block8.grow_pages(_handle(library), pool._record, table, lens, more, tokens), library, "cbs_grow_pages")
 

@@ -96,7 +96,11 @@ typedef struct cbs_page_pool {
  * the stack, as long as there are enough: the first that lacks some, and all after it, are left as
  * they are, as is (alone) one that would pass its row of the table or whose tokens pass `tokens`.
  * Their tokens, and those behind the last sequence's, get the slot -1 and the position 0; where a page
- * of the table or the stack lies outside the pool, the slot is -1.  counts[0] then holds the pages that are
+ * of the table or the stack lies outside the pool, the slot is -1.  The tokens of a sequence that is left lie between its
+ * starts all the same, and cbs_paged_attention, which goes by lens and knows no slots, takes them for its
+ * last old tokens: what it gives for a row whose slot is -1 stands for no token and is not to be used (the slots
+ * say on the device which rows those are; the other rows, and what the cache holds, are as they should be, and the
+ * tokens can be brought again when there is room).  counts[0] then holds the pages that are
  * left, counts[1] how many more all sequences that fit would have taken, counts[2] how many sequences with new tokens were
  * left.  starts end at `tokens`.
  * batch <= 65536, tokens <= 2^30, pages * page_size < 2^31.  Outputs must not overlap each other or
