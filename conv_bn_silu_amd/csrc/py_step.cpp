@@ -56,7 +56,7 @@ PyObject *add_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (a[3] != Py_None) {
             const at::Tensor &r = tensor(a[3], "residual", {x.scalar_type(), at::kFloat}, &x);
             if (r.sizes() != x.sizes()) refuse(PyExc_ValueError, "residual must have the shape of x");
-            sum = output(a[7], x.sizes(), r);
+            sum = output(a[7], x.sizes(), r, "sum_out");
             residual = rows_of(r, K);
         } else if (a[7] != Py_None) {
             refuse(PyExc_ValueError, "sum_out needs a residual");

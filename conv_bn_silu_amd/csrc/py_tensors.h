@@ -84,10 +84,10 @@ inline void contiguous(const at::Tensor &t, at::IntArrayRef shape, const char *w
     for (size_t i = 0; i < shape.size(); ++i) s += (i ? ", " : "") + std::to_string(shape[i]);
     refuse(PyExc_ValueError, s + ")");
 }
-inline at::Tensor output(PyObject *out, at::IntArrayRef shape, const at::Tensor &like) {
+inline at::Tensor output(PyObject *out, at::IntArrayRef shape, const at::Tensor &like, const char *what = "out") {
     if (out == Py_None) return at::empty(shape, like.options().requires_grad(false));
-    const at::Tensor &t = tensor(out, "out", {like.scalar_type()}, &like);
-    contiguous(t, shape, "out");
+    const at::Tensor &t = tensor(out, what, {like.scalar_type()}, &like);
+    contiguous(t, shape, what);
     return t;
 }
 inline at::Tensor workspace(int64_t bytes, const at::Tensor &like) {
