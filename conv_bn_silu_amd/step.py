@@ -4,7 +4,7 @@ the root-mean-square norm, rotary positions, and the cache's pages by the sequen
 lengths.
 
 As in ``block8``, every step runs in the HIP kernels, on the current stream; PyTorch
-supplies memory and streams; nothing is read back to the host, so that a whole step
+supplies memory and streams (and copies inputs whose rows the kernels cannot read in place); nothing is read back to the host, so that a whole step
 can be captured in a graph.  Forward only: inputs that require gradients or carry tangents are refused.
 """
 from __future__ import annotations
@@ -44,7 +44,9 @@ def add_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, int8: bool = 
     """y = h * weight / sqrt(mean(h^2) + eps) over the last axis, with h = x + residual.
 
     x: [..., K] float32, bfloat16 or float16; weight: [K] of x's type or float32, or None
-    for ones; residual: of x's shape, of x's type or float32, or None (then h is x).
+    for ones; residual: of x's shape, of x's type or float32, or None (then h is x).  x and the residual are read in
+    place where they are rows one distance apart, each contiguous (a slice of a wider matrix's columns, say); other
+    layouts, as some heads of a [tokens, heads, dim] tensor, are copied by PyTorch first.
     int8: give y as ``Rows8`` for ``int8_linear`` (quantised without a rounding to x's type in between).
 
     Returns y, of x's type; with a residual (y, h), h of the residual's type.  sum_out may be the
@@ -169,7 +171,8 @@ def grow_pages(pool: PagePool, table, lens, more, tokens: int, library: Library 
 
     Returns (starts, slots, positions): int32 [batch + 1], where each sequence's new tokens begin in the
     batch, and int32 [tokens], the new tokens' slots in the cache and their positions; what ``rotary_cache_write`` and
-    ``paged_attention`` take.  Sequences grow in order as long as there are pages; the first that lacks
+    ``paged_attention`` take.  They lie in one allocation: who keeps one of them for long keeps the memory of all
+    three, and clones it instead.  Sequences grow in order as long as there are pages; the first that lacks
     some, and all after it, are left as they are, as is one that would pass its row of the table or whose tokens pass
     `tokens`.  Tokens without a place (and padding) have slot -1 and position 0.  ``pool.report()`` says how it went.
 
