@@ -41,14 +41,14 @@ __device__ __forceinline__ double reciprocal_root(double s) {
     return s == INFINITY ? 0.0 : better;
 }
 
-// 8 values of a row from k on.  FULL: K is a whole number of 8s, so that nothing is ragged.
+// 8 values of a row from k on.  FULL: K is a whole number of 8s, so that nothing is ragged (what is does not stream).
 template <bool FULL, bool STREAM, typename T> __device__ __forceinline__ Held<T> take(const T *row, int k, int K) {
     if constexpr (FULL) return k < K ? Held<T>::template load<STREAM>(row + k) : Held<T>{};
-    else return Held<T>(load_chunk<STREAM>(row, k, K));
+    else return Held<T>(load_chunk(row, k, K));
 }
 template <bool FULL, bool STREAM, typename T> __device__ __forceinline__ void put(T *row, int k, int K, const Held<T> &v) {
-    if constexpr (FULL) store_held<STREAM>(row + k, v);
-    else v.template store<STREAM>(row, k, K);
+    if constexpr (FULL) v.template store<STREAM>(row + k);
+    else v.store_chunk(row, k, K);
 }
 
 // 8 weights on their way: they are asked for before the sum of squares, and wanted after it.  Wide ones beside

@@ -245,7 +245,7 @@ __device__ __forceinline__ void rotary_side_any(const RotaryParams &p, int block
     uint32_t next_slot = 0;
     auto take = [&](int i) {
         const int t = (int)by_heads.div((uint32_t)i), h = i - t * heads;
-        next = Held<T>(load_chunk<false>(from + t * token_step + h * head_step, d, a.dim));
+        next = Held<T>(load_chunk(from + t * token_step + h * head_step, d, a.dim));
         if constexpr (SIDE != 0) next_slot = (uint32_t)a.slots[token0 + t];
     };
     if (team < tasks) take(team);
@@ -290,7 +290,7 @@ __device__ __forceinline__ void rotary_side_any(const RotaryParams &p, int block
         }
         if constexpr (SIDE == 0) {
             T *const to = (T *)a.q_out + token0 * a.out_token + t * a.out_token + h * a.out_head;
-            if (d < a.dim) Held<T>(x).template store<false>(to, d, a.dim);
+            if (d < a.dim) Held<T>(x).store_chunk(to, d, a.dim);
         } else {
             if (slot >= p.slots) continue;  // negative slots are large numbers here
             const int64_t line = cache_line(p, slot, h);

@@ -11,45 +11,22 @@ namespace cbs {
 
 constexpr int64_t kCached = 256 << 20;  // bytes that the memory-side cache holds
 
-// As Value's, of tensors that are read and written once: they take no room in the caches that others want.
-template <typename T> struct Streamed {
-    static __device__ __forceinline__ u32x4 load(const void *p) {
-        typedef u32x4 __attribute__((aligned(1))) any;
-        return __builtin_nontemporal_load((const any *)p);
-    }
-    static __device__ __forceinline__ void store(void *p, u32x4 v) {
-        typedef u32x4 __attribute__((aligned(1))) any;
-        __builtin_nontemporal_store(v, (any *)p);
-    }
-    static __device__ __forceinline__ f32x8 load8(const T *p) {
-        if constexpr (sizeof(T) == 4) {
-            const f32x4 a = __builtin_bit_cast(f32x4, load(p)), b = __builtin_bit_cast(f32x4, load(p + 4));
-            return f32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        } else {
-            return __builtin_convertvector(__builtin_bit_cast(typename Value<T>::x8, load(p)), f32x8);
-        }
-    }
-    static __device__ __forceinline__ void store8(T *p, f32x8 v) {
-        if constexpr (sizeof(T) == 4) {
-            store(p, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
-            store(p + 4, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}));
-        } else {
-            store(p, __builtin_bit_cast(u32x4, __builtin_convertvector(v, typename Value<T>::x8)));
-        }
-    }
+// 16 bytes at any address, of tensors that are read and written once: they take no room in the caches that others want.
+struct Streamed {
+    typedef u32x4 __attribute__((aligned(1))) any;
+    static __device__ __forceinline__ u32x4 load(const void *p) { return __builtin_nontemporal_load((const any *)p); }
+    static __device__ __forceinline__ void store(void *p, u32x4 v) { __builtin_nontemporal_store(v, (any *)p); }
 };
 
 // 8 values from k on, zeros from K on.
-template <bool STREAM, typename T> __device__ __forceinline__ f32x8 load_chunk(const T *row, int k, int K) {
+template <typename T> __device__ __forceinline__ f32x8 load_chunk(const T *row, int k, int K) {
     f32x8 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (k + 8 <= K) return STREAM ? Streamed<T>::load8(row + k) : Value<T>::load8(row + k);
+    if (k + 8 <= K) return Value<T>::load8(row + k);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (k + i < K) x[i] = Value<T>::load1(row + k + i);
     return x;
 }
-template <typename T> struct Held;
-template <bool STREAM, typename T> __device__ __forceinline__ void store_held(T *p, const Held<T> &h);
 
 // 8 values as T holds them.
 template <typename T> struct Held {
@@ -59,12 +36,8 @@ template <typename T> struct Held {
         Held h;
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            h.raw[i] = STREAM ? Streamed<T>::load((const char *)p + 16 * i) : ((const Any16 *)p)[i].v;
+            h.raw[i] = STREAM ? Streamed::load((const char *)p + 16 * i) : ((const Any16 *)p)[i].v;
         return h;
-    }
-    __device__ __forceinline__ explicit Held(const u32x4 (&v)[sizeof(T) / 2]) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) raw[i] = v[i];
     }
     __device__ __forceinline__ explicit Held(f32x8 v) {
         if constexpr (sizeof(T) == 4) {
@@ -82,23 +55,22 @@ template <typename T> struct Held {
             return __builtin_convertvector(__builtin_bit_cast(typename Value<T>::x8, raw[0]), f32x8);
         }
     }
+    template <bool STREAM> __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            if constexpr (STREAM) Streamed::store((char *)p + 16 * i, raw[i]);
+            else ((Any16 *)p)[i].v = raw[i];
+        }
+    }
     // To row[k ..], as far as K.
-    template <bool STREAM> __device__ __forceinline__ void store(T *row, int k, int K) const {
-        if (k + 8 <= K) return store_held<STREAM>(row + k, *this);
+    __device__ __forceinline__ void store_chunk(T *row, int k, int K) const {
+        if (k + 8 <= K) return store<false>(row + k);
         const f32x8 v = get();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (k + i < K) Value<T>::store1(row + k + i, v[i]);
     }
 };
-
-template <bool STREAM, typename T> __device__ __forceinline__ void store_held(T *p, const Held<T> &h) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-        if constexpr (STREAM) Streamed<T>::store((char *)p + 16 * i, h.raw[i]);
-        else ((Any16 *)p)[i].v = h.raw[i];
-    }
-}
 
 // The value of the lane that the control names; `old` where there is none or the mask leaves the row out.
 template <int CTRL, int ROWS = 15> __device__ __forceinline__ uint32_t lane_from(uint32_t old, uint32_t v) {
