@@ -18,8 +18,8 @@
 //   128 x 1024 x 8192    4 parts   17.3   1.7
 // The pass over x takes 4 us of it for few rows, 5 to 8 for 256 to 1024 and 47 for 8192 x 8192.
 // Rows that come in 8 bits spare it: a norm (add_rms_norm) and the layer, us, with the values in 16 bits between them and with
-// the rows in 8: 1 x 4096 x 4096 9.7 and 9.3, 16 x 4096 x 4096 12.6 and 9.6, 1024 x 4096 x 4096 39 and 35,
-// 8192 x 8192 x 8192 629 and 587.
+// the rows in 8: 1 x 4096 x 4096 11.0 and 10.8, 16 x 4096 x 4096 14.8 and 11.0, 1024 x 4096 x 4096 39 and 35,
+// 8192 x 8192 x 8192 590 and 581.
 // 1024 x 4096 x 4096 has 256 tiles of 128, one to a CU: 25 us for 32 steps with four waves to feed a CU's matrix
 // pipes, where 256-tiles (64 of them) would leave three CUs of four idle.
 #include <hip/hip_runtime.h>

@@ -8,12 +8,13 @@
 // Rows beyond 8192 take 16 values a lane, those beyond 16384 read h a second time.  What the memory-side cache cannot
 // hold passes by the caches (180 -> 170 us; outputs in 8 bits stay, for the layer reads them: 8192 x 8192 with
 // what is read passing by as well 220 us into a layer of 1024, without 214), and eight workgroups of neighbouring rows
-// share an XCD (172 -> 169).  Together 170 us, 6.3 TB/s.
-//   Rows of 1024 (131072 of them) 171 us for 170, of 256 (300000) 98 for 98, of 128 (a million, no residual) 85
-//   for 85; 16384 wide 173 for 170; 32768 wide 209 for 170; one row of 4096: 2.8 us on the GPU, 5 to 6 a call.
-// With 8 bits the vector unit counts as well (450 instructions for a lane's 8 values at first, 87% of the time):
-// sizes of whole 8s have no ragged ends, and codes come out of one fused addition each.  8192 x 8192, bf16 with
-// residual: 104 -> 93 us (537 MB: 75), of 16384 253 -> 168 (149); residual in fp32 118 (738 MB: 117).
+// share an XCD (172 -> 169).  Together 171 us, 6.3 TB/s.
+//   Rows of 1024 (131072 of them) 170 us for 170, of 256 (300000) 98 for 98, of 128 (a million, no residual) 87
+//   for 85; 16384 wide 174 for 170; 32768 wide 207 for 170; one row of 4096: 2.3 us on the GPU, 5 to 6 a call.
+//   Widths in no whole 8s are guarded access by access and do not pass by the caches: 8191 wide 294 for 170.
+// With 8 bits the vector unit counts as well (451 instructions for a lane's 8 values at first, 87% of the cycles, 413
+// and 85% now): sizes of whole 8s have no ragged ends, and codes come out of one fused addition each.  8192 x 8192, bf16 with
+// residual: 104 -> 94 us (470 MB: 75), of 16384 253 -> 170 (149); residual in fp32 127 (738 MB: 117); 8191 wide 170 (75).
 //
 // Squares are summed in 64 bits: no row of finite numbers overflows or vanishes on the way.
 #include <hip/hip_runtime.h>

@@ -9,8 +9,8 @@
 // is the same the other way round (release; count_back and move_back).
 //
 // Bound by latency: a launch, the lengths, two sums over the workgroup, a page of the stack.  64 sequences with a
-// token each: 3.0 us on the GPU, and 2.7 to give them back (with the search for every token, and sums through LDS,
-// 6.8 and 4.0); the two calls take the host 7.5.  1024 prompts, 2.1 million tokens: 4 and 9 us, given back 6.6 (16 MB, which a
+// token each: 3.0 us on the GPU, and 2.8 to give them back (with the search for every token, and sums through LDS,
+// 6.8 and 4.0); the two calls take the host 7.5.  1024 prompts, 2.1 million tokens: 4 and 9 us, given back 3 and 4 (16 MB, which a
 // large copy would write in 3).
 #include <hip/hip_runtime.h>
 
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void grow(const PagesParams p) {
 }
 
 // 1024 tokens to a workgroup of 256.  Its first two waves look for the sequences of the first and the last of
-// them, 64 ways at a time.  (All sequences into LDS at once, where there are few workgroups: 6.8 us, so 6.4.)
+// them, 64 ways at a time.  (All sequences into LDS at once, where there are few workgroups, took 0.4 us more.)
 __global__ __launch_bounds__(256) void place(const PagesParams p) {
     __shared__ int ends[2];
     const PagesArgs &a = p.a;

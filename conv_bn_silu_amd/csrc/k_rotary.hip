@@ -7,13 +7,14 @@
 // angles out once, into LDS, while its first rows are on their way.
 //
 // Bound by HBM: every row is read once and written once.  32768 tokens, 32 heads over 8, dim 128, bf16 into
-// 8 bits: 128 us, 5.8 TB/s (740 MB; a large copy: 6.3 TB/s, 117 us).  Queries, keys and values go to different
+// 8 bits: 128 us, 5.8 TB/s (741 MB; a large copy: 6.3 TB/s, 118 us).  Queries, keys and values go to different
 // workgroups, whose addresses and branches are then the same for all lanes (a workgroup with all rows of
 // a token, each lane looking up its own: 185 us, 250 vector instructions a row of 16 lanes' values); a team takes two rows at
-// most, one after the other (eight: 146).  Other forms, us and what a copy would take: into 16 bits 145, 128;
-// fp32 into 8 bits 267, 224; dim 64 134, 101; dim 256 130, 117; 8 heads over 8 62, 53; 8192 tokens 37, 29; of 40 heads
-// without a cache 32, 27; 5001 ragged ones 10, 6; one or 64 tokens 3 on the GPU, 8 a call.  Pairs that are no whole 8
-// make smaller pieces: dim 80 with 20 pairs 133, 60; dim 100 with 50 120, 67 (any numbers, through LDS: 195 and 238).
+// most, one after the other (eight: 146).  Other forms of 32768 tokens, us and what a copy would take: into 16 bits 150, 128;
+// fp32 into 8 bits 271, 224; into 8 bits 64 heads over 8 of dim 64 134, 102, 16 over 4 of dim 256 130, 117, 8 over 8 of dim 128
+// 62, 54.  8192 tokens 33, 29, of 40 heads without a cache 29, 27; 5001 ragged ones (15 over 5, dim 80, fp16) 10, 6; 64 tokens
+// 4.7 on the GPU, 8 a call.  Pairs that are no whole 8s make smaller pieces: 24 heads over 8 of dim 80, 20 pairs, into 8
+// bits 134, 60; 32 of dim 100, 50 pairs, without a cache 99, 67 (odd numbers of pairs, through LDS: 25 197, 49 168).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
