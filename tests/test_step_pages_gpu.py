@@ -158,3 +158,52 @@ def test_growth_past_runs_of_idle_sequences(ops):
             ops.release_pages(pool, table, lens, keep)
     print("idle between %.3f ms, behind %.3f ms" % (min(times[:5]), min(times[5:])))
     assert min(times[:5]) < 20 * min(times[5:])
+
+
+@pytest.mark.parametrize("shape", [(9, 20, 6), (60, 1000, 700), (3, 30000, 20011), (1500, 60, 50), (4500, 30, 23)], ids=str)
+def test_pages_in_a_graph(ops, shape):
+    """Growth and giving back captured once and replayed, with holes made in between and other work beside, against the same
+    calls by themselves."""
+    n, width, per = shape
+    say("[pages graph]", shape)
+    page, tokens = 4, n * per * 4
+    more = torch.full((n,), per * 4, dtype=I32, device="cuda")
+    more[::3] -= 5
+    keep = torch.arange(n, dtype=I32, device="cuda") % 7
+    hole = torch.rand(n, width, device="cuda", generator=torch.Generator(device="cuda").manual_seed(n)) < 0.2
+    lost = torch.zeros((), dtype=I32, device="cuda")
+
+    def state():
+        return [ops.PagePool.full(n * per + 9, page), torch.full((n, width), -1, dtype=I32, device="cuda"),
+                torch.zeros(n, dtype=I32, device="cuda")]
+
+    def turn(pool, table, lens):
+        got = ops.grow_pages(pool, table, lens, more, tokens)
+        table.masked_fill_(hole, -1)
+        ops.release_pages(pool, table, lens, keep)
+        return got
+
+    eager, s = state(), state()
+    turn(*eager), turn(*s)
+    graph = torch.cuda.CUDAGraph()
+    before = [t.clone() for t in (s[0].free, s[0].counts, *s[1:])]
+    with torch.cuda.graph(graph):
+        out = turn(*s)
+    for t, v in zip((s[0].free, s[0].counts, *s[1:]), before):
+        t.copy_(v)
+    for i in range(5):
+        graph.replay()
+        want = turn(*eager)
+        lost += eager[0].counts[2]
+        torch.cuda.synchronize()
+        for a, b in zip((*want, eager[0].free, eager[0].counts, *eager[1:]), (*out, s[0].free, s[0].counts, *s[1:])):
+            assert torch.equal(a, b), i
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = turn(*eager)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip((*want, eager[0].free, eager[0].counts, *eager[1:]), (*out, s[0].free, s[0].counts, *s[1:])):
+        assert torch.equal(a, b)
+    assert int(lost) > 0  # holes are pages lost, and the pool ran short
